@@ -19,14 +19,19 @@
 #include <thread>
 #include <vector>
 
-#include "../../include/engram.h"
-#include "engram_internal.h"
+#include "api_internal.h"
 
 using namespace engram;
 
 namespace {
 
 thread_local std::string g_last_error;
+
+constexpr uint32_t kSessionMagic = 0x53474E45u;  // "ENGS"
+
+}  // namespace
+
+namespace engram {
 
 engram_status fail(engram_status st, const std::string& msg) {
     g_last_error = msg;
@@ -40,11 +45,6 @@ engram_status cuda_fail(cudaError_t e, const char* what) {
     return fail(ENGRAM_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-constexpr uint32_t kSessionMagic = 0x53474E45u;  // "ENGS"
-
-}  // namespace
-
-namespace engram {
 // Message for engram_last_error() from the library's other translation units.
 void set_last_error(const std::string& msg) { g_last_error = msg; }
 }  // namespace engram
@@ -123,44 +123,6 @@ uint64_t layer_multiplier(uint64_t seed, uint32_t j, uint32_t vc) {
 
 }  // namespace
 
-struct LayerState {
-    std::vector<uint64_t> mult;    // [nb][4]
-    std::vector<uint64_t> prime;   // [nb]
-    std::vector<uint64_t> offset;  // [nb]
-    uint64_t rows = 0;
-    bool bound = false;
-    engram_layer_weights w{};
-    CUtensorMap tm_wkv{};          // the caller's BF16 wkv
-    CUtensorMap tm_wkv_half{};     // the same with 128-row boxes (CTA-pair kernels)
-    // FP16 operand path of the fused kernels (see engram_layer_info)
-    bool f16 = false;
-    uint16_t* wkv_f16 = nullptr;   // library-owned copy, wkv x 2^wkv_exp
-    float* wqk = nullptr;          // library-owned w_q * w_k [hc][d], made at bind
-    CUtensorMap tm_wkv_f16{};
-    CUtensorMap tm_wkv_f16_2k{};   // the tiled FP16 copy with 256-row boxes (2 k-blocks)
-    int wkv_exp = 0;
-    int a_exp_shift = 0;
-    uint32_t scale_min = 0, scale_max = 0;
-    bool bucket_gather = false;    // whole 256-wide rows gathered once per tile and bucket
-    bool table_bf16 = false;       // BF16 rows without scales (ENGRAM_BIND_TABLE_BF16)
-    // bound to a shard of the table (engram_layer_bind_shard): rows
-    // [row_lo, row_lo + shard_rows) of the layer's table
-    bool shard = false;
-    uint64_t row_lo = 0, shard_rows = 0;
-};
-
-struct engram_ctx {
-    engram_ctx_desc desc{};
-    std::vector<uint64_t> seeds, bases;
-    std::vector<uint32_t> map;
-    int nb = 0, K = 0, N = 0;
-    std::vector<LayerState> layers;
-    uint32_t* d_err = nullptr;  // [0] error word, [1..3] bind-time scan results
-    int device = -1;
-    long long wait_limit_ns = 4000000000LL;
-    int starve_b = 0;
-};
-
 struct engram_session {
     const engram_ctx* ctx;
     uint32_t hist[3];  // c_{t-1}, c_{t-2}, c_{t-3} of the next position
@@ -170,8 +132,9 @@ struct engram_session {
 
 namespace {
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+}  // namespace
+
+namespace engram {
 
 engram_status check_layer(const engram_ctx* ctx, int layer, bool need_bound) {
     if (!ctx) return fail(ENGRAM_EINVAL, "null context");
@@ -181,16 +144,33 @@ engram_status check_layer(const engram_ctx* ctx, int layer, bool need_bound) {
     return ENGRAM_OK;
 }
 
-// Calls that index the layer's table with global row numbers need all of it.
-engram_status check_full_table(const engram_ctx* ctx, int layer) {
-    if (ctx->layers[layer].shard)
-        return fail(ENGRAM_ESTATE, "layer bound to a table shard: its rows come through "
-                                   "engram_shard_gather_raw and engram_stage_raw_rows");
+engram_status ensure_device_word(engram_ctx* ctx, int dev) {
+    if (ctx->d_err) return ENGRAM_OK;
+    cudaError_t e = cudaMalloc(&ctx->d_err, 4 * sizeof(uint32_t));
+    if (e != cudaSuccess) {
+        ctx->d_err = nullptr;
+        return fail(ENGRAM_ENOMEM, "cudaMalloc of the error word");
+    }
+    e = cudaMemset(ctx->d_err, 0, 4 * sizeof(uint32_t));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
+    ctx->device = dev;
     return ENGRAM_OK;
 }
 
 engram_status check_T(int64_t T) {
     if (T < 0 || T > (int64_t)1 << 24) return fail(ENGRAM_EINVAL, "T must be in [0, 2^24]");
+    return ENGRAM_OK;
+}
+
+}  // namespace engram
+
+namespace {
+
+// Calls that index the layer's table with global row numbers need all of it.
+engram_status check_full_table(const engram_ctx* ctx, int layer) {
+    if (ctx->layers[layer].shard)
+        return fail(ENGRAM_ESTATE, "layer bound to a table shard: its rows come through "
+                                   "engram_shard_gather_raw and engram_stage_raw_rows");
     return ENGRAM_OK;
 }
 
@@ -494,23 +474,6 @@ engram_status engram_layer_set_multipliers(engram_ctx* ctx, int layer, const uin
     std::copy(mult, mult + ctx->nb * 4, ctx->layers[layer].mult.begin());
     return ok();
 }
-
-namespace {
-// The context's device word (error word and scan results), allocated at the
-// first bind or scan on device dev.
-engram_status ensure_device_word(engram_ctx* ctx, int dev) {
-    if (ctx->d_err) return ENGRAM_OK;
-    cudaError_t e = cudaMalloc(&ctx->d_err, 4 * sizeof(uint32_t));
-    if (e != cudaSuccess) {
-        ctx->d_err = nullptr;
-        return fail(ENGRAM_ENOMEM, "cudaMalloc of the error word");
-    }
-    e = cudaMemset(ctx->d_err, 0, 4 * sizeof(uint32_t));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset");
-    ctx->device = dev;
-    return ENGRAM_OK;
-}
-}  // namespace
 
 engram_status engram_scale_range(engram_ctx* ctx, const uint8_t* scales, uint64_t n,
                                  uint32_t* scale_min, uint32_t* scale_max) {
