@@ -39,6 +39,11 @@ EXPORTS = (
     "engram_layer_bind_shard", "engram_scale_range", "engram_hash_by_bucket",
     "engram_raw_row_bytes", "engram_host_table_alloc", "engram_host_table_free",
     "engram_shard_gather_raw", "engram_stage_raw_rows",
+    "engram_embed", "engram_embed_grad", "engram_embed_grad_workspace_bytes",
+    "engram_gate_checkpoint", "engram_gate_backward", "engram_gate_backward_checkpoint",
+    "engram_gate_backward_workspace_bytes", "engram_project_backward",
+    "engram_project_backward_workspace_bytes", "engram_loss", "engram_loss_workspace_bytes",
+    "engram_loss_backward", "engram_loss_backward_workspace_bytes",
     "engram_sync", "engram_ctx_set_wait_limit", "engram_debug_starve_operand",
     "engram_last_error",
 )
@@ -63,6 +68,7 @@ class CtxDesc(C.Structure):
 BIND_BF16_OPERANDS = 1
 BIND_TABLE_BF16 = 2
 KV_F32, KV_BF16 = 0, 1  # engram_prepass: kv as fp32, or rounded once to BF16
+EMBED_F32, EMBED_BF16 = 0, 1  # engram_embed: the table's type
 
 
 class LayerWeights(C.Structure):
@@ -92,6 +98,7 @@ def lib() -> C.CDLL:
                                "(engram_gram_conditional_gb300.build.build())")
         L = C.CDLL(LIB_PATH)
         vp, i64, st = C.c_void_p, C.c_int64, C.c_int
+        u32, u64, f32 = C.c_uint32, C.c_uint64, C.c_float
         sig = {
             "engram_ctx_create": [C.POINTER(CtxDesc), vp, C.POINTER(vp)],
             "engram_ctx_destroy": [vp],
@@ -131,13 +138,30 @@ def lib() -> C.CDLL:
             "engram_shard_gather_raw": [vp, C.c_int, vp, i64, vp, vp],
             "engram_stage_raw_rows": [vp, C.c_int, vp, vp, i64, vp, vp],
             "engram_debug_starve_operand": [vp, C.c_int],
+            "engram_embed": [vp, vp, C.c_int, u64, u32, vp, i64, f32, u32, vp, vp],
+            "engram_embed_grad": [vp, u64, u32, vp, i64, f32, u32, vp, vp, vp, vp, C.c_int, vp, vp],
+            "engram_gate_checkpoint": [vp, C.c_int, vp, C.c_int, vp, i64, vp, vp, vp, vp, vp, vp],
+            "engram_gate_backward": [vp, C.c_int, vp, C.c_int, vp, vp, i64, vp, vp, vp, vp, vp, vp,
+                                     vp],
+            "engram_gate_backward_checkpoint": [vp, C.c_int, vp, vp, vp, i64, vp, vp, vp, vp, vp,
+                                                vp, vp],
+            "engram_project_backward": [vp, C.c_int, vp, vp, i64, vp, vp, vp, vp],
+            "engram_loss": [vp, vp, vp, u32, u32, vp, i64, vp, vp, vp, vp],
+            "engram_loss_backward": [vp, vp, vp, u32, u32, vp, i64, vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = st
-        for name in ("engram_workspace_bytes", "engram_forward_staged_workspace_bytes"):
+        for name in ("engram_workspace_bytes", "engram_forward_staged_workspace_bytes",
+                     "engram_gate_backward_workspace_bytes",
+                     "engram_project_backward_workspace_bytes"):
             getattr(L, name).argtypes = [vp, i64]
+            getattr(L, name).restype = C.c_size_t
+        for name, args in (("engram_embed_grad_workspace_bytes", [i64, u64, u32]),
+                           ("engram_loss_workspace_bytes", [i64, u32, u32]),
+                           ("engram_loss_backward_workspace_bytes", [i64, u32, u32])):
+            getattr(L, name).argtypes = args
             getattr(L, name).restype = C.c_size_t
         L.engram_raw_row_bytes.argtypes = [vp]
         L.engram_raw_row_bytes.restype = C.c_size_t
@@ -395,6 +419,81 @@ def engram_shard_gather_raw(ctx, layer, d_ids, n, d_raw, stream=None):
 def engram_stage_raw_rows(ctx, layer, d_rows_bm, d_raw_bm, T, d_workspace, stream=None):
     _check(lib().engram_stage_raw_rows(ctx, layer, _ptr(d_rows_bm), _ptr(d_raw_bm), T,
                                        _ptr(d_workspace), _stream(stream)))
+
+
+# ---- training ----------------------------------------------------------------------------
+
+def engram_embed(ctx, d_table, table_format, rows, dim, d_ids, n, scale, copies, d_out,
+                 stream=None):
+    _check(lib().engram_embed(ctx, _ptr(d_table), int(table_format), rows, dim, _ptr(d_ids), n,
+                              scale, copies, _ptr(d_out), _stream(stream)))
+
+
+def engram_embed_grad_workspace_bytes(n: int, rows: int, dim: int) -> int:
+    return int(lib().engram_embed_grad_workspace_bytes(n, rows, dim))
+
+
+def engram_embed_grad(ctx, rows, dim, d_ids, n, scale, copies, d_dout, d_unique, d_count, d_grad,
+                      accumulate, d_workspace, stream=None):
+    _check(lib().engram_embed_grad(ctx, rows, dim, _ptr(d_ids), n, scale, copies, _ptr(d_dout),
+                                   _ptr(d_unique), _ptr(d_count), _ptr(d_grad), int(accumulate),
+                                   _ptr(d_workspace), _stream(stream)))
+
+
+def engram_gate_checkpoint(ctx, layer, d_kv, kv_format, d_windows, T, d_hidden, d_hidden_out,
+                           d_gates, d_codes, d_scales, stream=None):
+    _check(lib().engram_gate_checkpoint(ctx, layer, _ptr(d_kv), int(kv_format), _ptr(d_windows), T,
+                                        _ptr(d_hidden), _ptr(d_hidden_out), _ptr(d_gates),
+                                        _ptr(d_codes), _ptr(d_scales), _stream(stream)))
+
+
+def engram_gate_backward_workspace_bytes(ctx, T: int) -> int:
+    return int(lib().engram_gate_backward_workspace_bytes(ctx, T))
+
+
+def engram_gate_backward(ctx, layer, d_kv, kv_format, d_hidden, d_windows, T, d_dout, d_dhidden,
+                         d_dkv, d_dwq, d_dwk, d_workspace, stream=None):
+    _check(lib().engram_gate_backward(ctx, layer, _ptr(d_kv), int(kv_format), _ptr(d_hidden),
+                                      _ptr(d_windows), T, _ptr(d_dout), _ptr(d_dhidden),
+                                      _ptr(d_dkv), _ptr(d_dwq), _ptr(d_dwk), _ptr(d_workspace),
+                                      _stream(stream)))
+
+
+def engram_gate_backward_checkpoint(ctx, layer, d_codes, d_scales, d_windows, T, d_dout, d_dhidden,
+                                    d_dkv, d_dwq, d_dwk, d_workspace, stream=None):
+    _check(lib().engram_gate_backward_checkpoint(ctx, layer, _ptr(d_codes), _ptr(d_scales),
+                                                 _ptr(d_windows), T, _ptr(d_dout), _ptr(d_dhidden),
+                                                 _ptr(d_dkv), _ptr(d_dwq), _ptr(d_dwk),
+                                                 _ptr(d_workspace), _stream(stream)))
+
+
+def engram_project_backward_workspace_bytes(ctx, T: int) -> int:
+    return int(lib().engram_project_backward_workspace_bytes(ctx, T))
+
+
+def engram_project_backward(ctx, layer, d_emb, d_dkv, T, d_demb, d_dwkv, d_workspace, stream=None):
+    _check(lib().engram_project_backward(ctx, layer, _ptr(d_emb), _ptr(d_dkv), T, _ptr(d_demb),
+                                         _ptr(d_dwkv), _ptr(d_workspace), _stream(stream)))
+
+
+def engram_loss_workspace_bytes(T: int, vocab: int, dim: int) -> int:
+    return int(lib().engram_loss_workspace_bytes(T, vocab, dim))
+
+
+def engram_loss(ctx, d_x, d_head, vocab, dim, d_labels, T, d_loss, d_lse, d_workspace, stream=None):
+    _check(lib().engram_loss(ctx, _ptr(d_x), _ptr(d_head), vocab, dim, _ptr(d_labels), T,
+                             _ptr(d_loss), _ptr(d_lse), _ptr(d_workspace), _stream(stream)))
+
+
+def engram_loss_backward_workspace_bytes(T: int, vocab: int, dim: int) -> int:
+    return int(lib().engram_loss_backward_workspace_bytes(T, vocab, dim))
+
+
+def engram_loss_backward(ctx, d_x, d_head, vocab, dim, d_labels, T, d_lse, d_dloss, d_dx, d_dhead,
+                         d_workspace, stream=None):
+    _check(lib().engram_loss_backward(ctx, _ptr(d_x), _ptr(d_head), vocab, dim, _ptr(d_labels), T,
+                                      _ptr(d_lse), _ptr(d_dloss), _ptr(d_dx), _ptr(d_dhead),
+                                      _ptr(d_workspace), _stream(stream)))
 
 
 def engram_ctx_set_wait_limit(ctx, ns: int):

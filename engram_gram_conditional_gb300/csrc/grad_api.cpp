@@ -1,0 +1,582 @@
+// Host side of the training operators of libengram.so: the embedding and its
+// gradient, the gate with an 8-bit checkpoint and its backward pass, the
+// projection's backward pass, and the large-vocabulary loss (include/engram.h).
+#include <algorithm>
+
+#include "api_internal.h"
+#include "grad_internal.h"
+
+using namespace engram;
+
+namespace {
+
+// Carves a workspace into 256-byte aligned parts; with a null base it only
+// counts bytes.
+struct Carver {
+    uint8_t* base;
+    size_t at = 0;
+    explicit Carver(void* p) : base(static_cast<uint8_t*>(p)) {}
+    template <class T>
+    T* take(size_t n) {
+        T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
+        at = (at + n * sizeof(T) + 255) & ~(size_t)255;
+        return p;
+    }
+};
+
+// The current device, and the context's device word on it (a context that has
+// no bound layer gets it here).
+engram_status train_device(engram_ctx* ctx) {
+    if (!ctx) return fail(ENGRAM_EINVAL, "null context");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (ctx->device >= 0 && ctx->device != dev)
+        return fail(ENGRAM_ESTATE, "context already bound on another device");
+    return ensure_device_word(ctx, dev);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- embedding -------------------------------------------------------------------------
+
+engram_status check_embed(uint64_t rows, uint32_t dim, int64_t n, uint32_t copies) {
+    if (rows < 1 || rows >= 0xFFFFFFFFull) return fail(ENGRAM_EINVAL, "rows must be in [1, 2^32 - 2]");
+    if (dim < 8 || dim % 8 || dim > 65536) return fail(ENGRAM_EINVAL, "dim must be a multiple of 8 in [8, 65536]");
+    if (n < 0 || n > (int64_t)1 << 30) return fail(ENGRAM_EINVAL, "n must be in [0, 2^30]");
+    if (copies < 1 || copies > 8) return fail(ENGRAM_EINVAL, "copies must be in [1, 8]");
+    return ENGRAM_OK;
+}
+
+struct EmbedWs {
+    uint32_t *keys0, *keys1, *vals0, *vals1, *hist, *digit_total, *block_heads, *barrier, *n_valid,
+        *segpos, *seg_start, *unique, *count;
+    float* partial;
+    size_t bytes;
+};
+
+EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
+    int passes, bits;
+    embed_sort_digits(rows, &passes, &bits);
+    const size_t blocks = embed_sort_blocks(n), bins = (size_t)1 << bits;
+    Carver c(p);
+    EmbedWs w{};
+    w.keys0 = c.take<uint32_t>(n);
+    w.keys1 = c.take<uint32_t>(n);
+    w.vals0 = c.take<uint32_t>(n);
+    w.vals1 = c.take<uint32_t>(n);
+    w.hist = c.take<uint32_t>(blocks * bins);
+    w.digit_total = c.take<uint32_t>(bins);
+    w.block_heads = c.take<uint32_t>(blocks);
+    w.barrier = c.take<uint32_t>(1);
+    w.n_valid = c.take<uint32_t>(1);
+    w.count = c.take<uint32_t>(1);
+    w.segpos = c.take<uint32_t>(n);
+    w.seg_start = c.take<uint32_t>(n + 1);
+    w.unique = c.take<uint32_t>(n);
+    const int64_t chunks = ceil_div(n, embed_rows_per_chunk(n, (int)dim, 1));
+    w.partial = c.take<float>((size_t)chunks * 2 * dim);
+    w.bytes = c.at;
+    return w;
+}
+
+// ---- gate ------------------------------------------------------------------------------
+
+GateTrain gate_args(const engram_ctx* ctx, int layer, const uint32_t* windows, int64_t T) {
+    GateTrain a{};
+    const LayerState& L = ctx->layers[layer];
+    a.T = T;
+    a.hc = (int)ctx->desc.hc;
+    a.d = (int)ctx->desc.d;
+    a.eps = (float)ctx->desc.eps;
+    a.windows = reinterpret_cast<const uint4*>(windows);
+    a.wqk = L.wqk;
+    a.wq = L.w.wq;
+    a.wk = L.w.wk;
+    return a;
+}
+
+size_t gate_backward_ws(GateTrain* a, void* p, int64_t T, int hc, int d) {
+    Carver c(p);
+    float4* f = c.take<float4>((size_t)T * hc);
+    float* part = c.take<float>((size_t)gate_backward_shares(std::max<int64_t>(T, 1), d) * hc * d);
+    if (a) {
+        a->factors = f;
+        a->dw_part = part;
+    }
+    return c.at;
+}
+
+engram_status gate_backward_call(const engram_ctx* ctx, GateTrain& a, int saved, void* ws,
+                                 cudaStream_t s) {
+    const size_t nw = (size_t)a.hc * a.d * sizeof(float);
+    if (a.T == 0) {
+        cudaError_t e = cudaSuccess;
+        if (a.dwq) e = cudaMemsetAsync(a.dwq, 0, nw, s);
+        if (e == cudaSuccess && a.dwk) e = cudaMemsetAsync(a.dwk, 0, nw, s);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "gate backward of no tokens");
+    }
+    gate_backward_ws(&a, ws, a.T, a.hc, a.d);
+    cudaError_t e = launch_gate_backward(a, saved, s);
+    if (e != cudaSuccess) return cuda_fail(e, "gate backward launch");
+    return ok();
+}
+
+// ---- products ----------------------------------------------------------------------------
+
+// One of the two gradient products of a launch.
+GradProblem product(int64_t M, int64_t N, int64_t reduce, bool a_mn, uint16_t* out) {
+    GradProblem q{};
+    q.m_units = (int)ceil_div(M, 2 * kBM);
+    q.n_tiles = (int)ceil_div(N, kBN);
+    q.kb = (int)ceil_div(reduce, kBK);
+    q.splits = 1;
+    q.a_mn = a_mn;
+    q.group_m = 8;
+    q.M = M;
+    q.N = N;
+    q.out = out;
+    return q;
+}
+
+// How often the long product's reduction is cut, so that its few tiles keep
+// every pair busy: not at all while one item costs no more than a pair's mean
+// share of the launch.
+int long_splits(const GradProblem& lng, const GradProblem* shrt) {
+    const double P = grad_pairs();
+    const double tiles = (double)lng.m_units * lng.n_tiles;
+    const double light = shrt ? (double)shrt->m_units * shrt->n_tiles * shrt->kb : 0.0;
+    int best = 1;
+    double best_t = 1e300;
+    for (int s = 1; s <= 8 && s <= lng.kb; ++s) {
+        const double item = (double)lng.kb / s;
+        const double rounds = (double)ceil_div((int64_t)(tiles * s), (int64_t)P);
+        const double mean = (tiles * lng.kb + light) / P;
+        // parking and adding a split's partial sums costs about a k-block per item
+        const double t = std::max(rounds * item, mean) + (s > 1 ? rounds * 2.0 + s : 0.0);
+        if (t < best_t * 0.98) {
+            best_t = t;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// ---- loss -------------------------------------------------------------------------------
+
+engram_status check_loss(uint32_t vocab, uint32_t dim, int64_t T) {
+    if (vocab < 1 || vocab > (1u << 30)) return fail(ENGRAM_EINVAL, "vocab must be in [1, 2^30]");
+    if (dim < 8 || dim % 8 || dim > 65536) return fail(ENGRAM_EINVAL, "dim must be a multiple of 8 in [8, 65536]");
+    return check_T(T);
+}
+
+int loss_group_m(uint32_t dim) {  // M units whose x rows (40 MB) stay in L2 beside the head
+    return (int)std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)40 << 20) / (512 * (int64_t)dim)));
+}
+
+// Vocabulary columns per piece of the backward pass: whole waves of z tiles
+// while dz [T][piece] stays within half of L2, and at least one wave.
+int64_t loss_piece(int64_t T, uint32_t vocab) {
+    const int64_t units = std::max<int64_t>(1, ceil_div(T, 2 * kBM)), P = grad_pairs();
+    const int64_t all = ceil_div(vocab, kBN);
+    const int64_t fit = ((int64_t)64 << 20) / (units * 2 * kBM * kBN * 2);  // tiles within 64 MB
+    int64_t waves = fit * units / P;
+    int64_t tiles = std::max<int64_t>(16, waves >= 1 ? waves * P / units : P / units);
+    tiles = std::min(std::max<int64_t>(1, tiles), all);
+    return tiles * kBN;
+}
+
+struct LossBackWs {
+    uint16_t* dz;
+    float* acc;
+    int splits;
+    size_t bytes;
+};
+GradProblem loss_dx(int64_t T, uint32_t dim, int64_t piece, uint16_t* out) {
+    GradProblem q = product(T, dim, piece, false, out);
+    q.a_tiled = (int)(piece / 64);
+    return q;
+}
+GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece, uint16_t* out) {
+    GradProblem q = product(cols, dim, T, true, out);
+    q.a_tiled = (int)(piece / 64);
+    q.n_fast = 1;
+    return q;
+}
+LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim) {
+    const int64_t piece = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
+    const GradProblem dx = loss_dx(T, dim, piece, nullptr);
+    const GradProblem dh = loss_dhead(T, dim, piece, piece, nullptr);
+    LossBackWs w{};
+    w.splits = long_splits(dx, &dh);
+    Carver c(p);
+    w.dz = c.take<uint16_t>((size_t)rows * piece);
+    w.acc = c.take<float>(w.splits > 1 || piece < vocab ? (size_t)w.splits * T * dim : 0);
+    w.bytes = c.at;
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+engram_status engram_embed(engram_ctx* ctx, const void* d_table, int table_format, uint64_t rows,
+                           uint32_t dim, const uint32_t* d_ids, int64_t n, float scale,
+                           uint32_t copies, uint16_t* d_out, void* stream) {
+    engram_status st = check_embed(rows, dim, n, copies);
+    if (st) return st;
+    if (!ctx) return fail(ENGRAM_EINVAL, "null context");
+    if (table_format != ENGRAM_EMBED_F32 && table_format != ENGRAM_EMBED_BF16)
+        return fail(ENGRAM_EINVAL, "unknown table format");
+    if (n == 0) return ok();
+    if (!d_table || !d_ids || !d_out || !aligned16(d_table) || !aligned4(d_ids) || !aligned16(d_out))
+        return fail(ENGRAM_EINVAL, "table, out (16-byte aligned) / ids");
+    if ((st = train_device(ctx))) return st;
+    cudaError_t e = launch_embed(d_table, table_format == ENGRAM_EMBED_F32, rows, (int)dim, d_ids, n,
+                                 scale, (int)copies, d_out, ctx->d_err, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "embed launch");
+    return ok();
+}
+
+size_t engram_embed_grad_workspace_bytes(int64_t n, uint64_t rows, uint32_t dim) {
+    if (check_embed(rows, dim, n, 1)) return 0;
+    return embed_ws(nullptr, n, rows, dim).bytes;
+}
+
+engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, const uint32_t* d_ids,
+                                int64_t n, float scale, uint32_t copies, const uint16_t* d_dout,
+                                uint32_t* d_unique, uint32_t* d_count, float* d_grad,
+                                int accumulate, void* d_workspace, void* stream) {
+    engram_status st = check_embed(rows, dim, n, copies);
+    if (st) return st;
+    if (!ctx) return fail(ENGRAM_EINVAL, "null context");
+    const bool dense = d_unique == nullptr;
+    if (accumulate != 0 && accumulate != 1) return fail(ENGRAM_EINVAL, "accumulate must be 0 or 1");
+    if (accumulate && !dense) return fail(ENGRAM_EINVAL, "only a dense gradient accumulates");
+    if (!d_grad || !aligned16(d_grad) || (!dense && (!d_count || !aligned4(d_unique))) ||
+        !aligned4(d_count))
+        return fail(ENGRAM_EINVAL, "grad (16-byte aligned) / unique / count");
+    if (n > 0 && (!d_ids || !d_dout || !d_workspace || !aligned4(d_ids) || !aligned16(d_dout) ||
+                  !aligned16(d_workspace)))
+        return fail(ENGRAM_EINVAL, "ids / dout, workspace (16-byte aligned)");
+    if ((st = train_device(ctx))) return st;
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    if (dense && !accumulate) e = cudaMemsetAsync(d_grad, 0, rows * dim * sizeof(float), s);
+    if (e == cudaSuccess && n == 0 && d_count) e = cudaMemsetAsync(d_count, 0, sizeof(uint32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "embed gradient clear");
+    if (n == 0) return ok();
+    const EmbedWs w = embed_ws(d_workspace, n, rows, dim);
+    EmbedSort a{};
+    a.ids = d_ids;
+    a.n = n;
+    a.rows = rows;
+    embed_sort_digits(rows, &a.passes, &a.digit_bits);
+    a.keys0 = w.keys0;
+    a.keys1 = w.keys1;
+    a.vals0 = w.vals0;
+    a.vals1 = w.vals1;
+    a.hist = w.hist;
+    a.digit_total = w.digit_total;
+    a.block_heads = w.block_heads;
+    a.barrier = w.barrier;
+    a.n_valid = w.n_valid;
+    a.segpos = w.segpos;
+    a.seg_start = w.seg_start;
+    a.unique = dense ? w.unique : d_unique;
+    a.count = d_count ? d_count : w.count;
+    a.err = ctx->d_err;
+    a.wait_limit_ns = ctx->wait_limit_ns;
+    e = launch_embed_sort(a, s);
+    if (e != cudaSuccess) return cuda_fail(e, "embed sort launch");
+    EmbedSum u{};
+    u.perm = a.passes & 1 ? w.vals1 : w.vals0;
+    u.segpos = w.segpos;
+    u.seg_start = w.seg_start;
+    u.unique = a.unique;
+    u.n_valid = w.n_valid;
+    u.dout = d_dout;
+    u.dim = (int)dim;
+    u.copies = (int)copies;
+    u.scale = scale;
+    u.dense = dense;
+    u.accumulate = accumulate;
+    u.grad = d_grad;
+    u.rows_per_chunk = embed_rows_per_chunk(n, (int)dim, (int)copies);
+    u.partial = w.partial;
+    e = launch_embed_sum(u, n, s);
+    if (e != cudaSuccess) return cuda_fail(e, "embed gradient launch");
+    return ok();
+}
+
+engram_status engram_gate_checkpoint(const engram_ctx* ctx, int layer, const void* d_kv,
+                                     int kv_format, const uint32_t* d_windows, int64_t T,
+                                     const uint16_t* d_hidden, uint16_t* d_hidden_out,
+                                     float* d_gates, uint8_t* d_codes, uint8_t* d_scales,
+                                     void* stream) {
+    engram_status st = check_layer(ctx, layer, true);
+    if (st || (st = check_T(T))) return st;
+    if (kv_format != ENGRAM_KV_F32 && kv_format != ENGRAM_KV_BF16)
+        return fail(ENGRAM_EINVAL, "kv_format");
+    if (T == 0) return ok();
+    if (!d_kv || !d_windows || !d_hidden || !d_hidden_out || !d_codes || !d_scales ||
+        !aligned16(d_kv) || !aligned16(d_windows) || !aligned16(d_hidden) ||
+        !aligned16(d_hidden_out) || !aligned16(d_codes) || !aligned16(d_scales))
+        return fail(ENGRAM_EINVAL, "kv / windows / hidden / codes / scales (16-byte aligned)");
+    GateTrain a = gate_args(ctx, layer, d_windows, T);
+    a.kv = d_kv;
+    a.hidden = d_hidden;
+    a.hidden_out = d_hidden_out;
+    a.gates = d_gates;
+    a.codes_out = d_codes;
+    a.scales_out = d_scales;
+    cudaError_t e = launch_gate_checkpoint(a, kv_format == ENGRAM_KV_F32, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "gate checkpoint launch");
+    return ok();
+}
+
+size_t engram_gate_backward_workspace_bytes(const engram_ctx* ctx, int64_t T) {
+    if (!ctx || check_T(T)) return 0;
+    return gate_backward_ws(nullptr, nullptr, T, (int)ctx->desc.hc, (int)ctx->desc.d);
+}
+
+engram_status engram_gate_backward(const engram_ctx* ctx, int layer, const void* d_kv,
+                                   int kv_format, const uint16_t* d_hidden,
+                                   const uint32_t* d_windows, int64_t T, const uint16_t* d_dout,
+                                   uint16_t* d_dhidden, uint16_t* d_dkv, float* d_dwq, float* d_dwk,
+                                   void* d_workspace, void* stream) {
+    engram_status st = check_layer(ctx, layer, true);
+    if (st || (st = check_T(T))) return st;
+    if (kv_format != ENGRAM_KV_F32 && kv_format != ENGRAM_KV_BF16)
+        return fail(ENGRAM_EINVAL, "kv_format");
+    if (T > 0 && (!d_kv || !d_hidden || !d_windows || !d_dout || !d_dhidden || !d_dkv ||
+                  !d_workspace || !aligned16(d_kv) || !aligned16(d_hidden) ||
+                  !aligned16(d_windows) || !aligned16(d_dout) || !aligned16(d_dhidden) ||
+                  !aligned16(d_dkv) || !aligned16(d_workspace)))
+        return fail(ENGRAM_EINVAL, "kv / hidden / windows / gradients / workspace (16-byte aligned)");
+    if (!aligned16(d_dwq) || !aligned16(d_dwk))
+        return fail(ENGRAM_EINVAL, "dwq / dwk (16-byte aligned)");
+    GateTrain a = gate_args(ctx, layer, d_windows, T);
+    a.kv = d_kv;
+    a.hidden = d_hidden;
+    a.dout = d_dout;
+    a.dhidden = d_dhidden;
+    a.dkv = d_dkv;
+    a.dwq = d_dwq;
+    a.dwk = d_dwk;
+    return gate_backward_call(ctx, a, kv_format == ENGRAM_KV_F32 ? kSavedF32 : kSavedBf16,
+                              d_workspace, (cudaStream_t)stream);
+}
+
+engram_status engram_gate_backward_checkpoint(const engram_ctx* ctx, int layer,
+                                              const uint8_t* d_codes, const uint8_t* d_scales,
+                                              const uint32_t* d_windows, int64_t T,
+                                              const uint16_t* d_dout, uint16_t* d_dhidden,
+                                              uint16_t* d_dkv, float* d_dwq, float* d_dwk,
+                                              void* d_workspace, void* stream) {
+    engram_status st = check_layer(ctx, layer, true);
+    if (st || (st = check_T(T))) return st;
+    if (T > 0 && (!d_codes || !d_scales || !d_windows || !d_dout || !d_dhidden || !d_dkv ||
+                  !d_workspace || !aligned16(d_codes) || !aligned16(d_scales) ||
+                  !aligned16(d_windows) || !aligned16(d_dout) || !aligned16(d_dhidden) ||
+                  !aligned16(d_dkv) || !aligned16(d_workspace)))
+        return fail(ENGRAM_EINVAL, "codes / scales / windows / gradients / workspace (16-byte aligned)");
+    if (!aligned16(d_dwq) || !aligned16(d_dwk))
+        return fail(ENGRAM_EINVAL, "dwq / dwk (16-byte aligned)");
+    GateTrain a = gate_args(ctx, layer, d_windows, T);
+    a.codes = d_codes;
+    a.scales = d_scales;
+    a.dout = d_dout;
+    a.dhidden = d_dhidden;
+    a.dkv = d_dkv;
+    a.dwq = d_dwq;
+    a.dwk = d_dwk;
+    return gate_backward_call(ctx, a, kSavedMx, d_workspace, (cudaStream_t)stream);
+}
+
+size_t engram_project_backward_workspace_bytes(const engram_ctx* ctx, int64_t T) {
+    if (!ctx || check_T(T) || T == 0) return 0;
+    const GradProblem demb = product(T, ctx->K, ctx->N, false, nullptr);
+    const GradProblem dw = product(ctx->N, ctx->K, T, true, nullptr);
+    // with or without the other product the cut may differ: room for either
+    const int splits = std::max(long_splits(demb, &dw), long_splits(demb, nullptr));
+    return splits > 1 ? (size_t)splits * T * ctx->K * sizeof(float) : 0;
+}
+
+engram_status engram_project_backward(const engram_ctx* ctx, int layer, const uint16_t* d_emb,
+                                      const uint16_t* d_dkv, int64_t T, uint16_t* d_demb,
+                                      uint16_t* d_dwkv, void* d_workspace, void* stream) {
+    engram_status st = check_layer(ctx, layer, true);
+    if (st || (st = check_T(T))) return st;
+    if (!aligned16(d_demb) || !aligned16(d_dwkv) || !aligned16(d_workspace))
+        return fail(ENGRAM_EINVAL, "demb / dwkv / workspace (16-byte aligned)");
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int64_t N = ctx->N, K = ctx->K;
+    if (T == 0) {
+        cudaError_t e = d_dwkv ? cudaMemsetAsync(d_dwkv, 0, (size_t)N * K * 2, s) : cudaSuccess;
+        return e == cudaSuccess ? ok() : cuda_fail(e, "project backward of no tokens");
+    }
+    if (!d_dkv || !aligned16(d_dkv) || (d_dwkv && (!d_emb || !aligned16(d_emb))))
+        return fail(ENGRAM_EINVAL, "emb / dkv (16-byte aligned)");
+    if (!d_demb && !d_dwkv) return ok();
+    const LayerState& L = ctx->layers[layer];
+    GradArgs a{};
+    a.err = ctx->d_err;
+    a.wait_limit_ns = ctx->wait_limit_ns;
+    CUtensorMap tm[4];
+    cudaError_t e = cudaSuccess;
+    if (d_dwkv) {
+        a.pr[1] = product(N, K, T, true, d_dwkv);
+        a.pr[1].n_fast = 1;
+        e = make_tma_16bit(&tm[2], d_dkv, T, N, 64, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[3], d_emb, T, K, 64, false);
+    }
+    if (d_demb && e == cudaSuccess) {
+        a.pr[0] = product(T, K, N, false, d_demb);
+        a.pr[0].splits = long_splits(a.pr[0], d_dwkv ? &a.pr[1] : nullptr);
+        if (a.pr[0].splits > 1) {
+            if (!d_workspace) return fail(ENGRAM_EINVAL, "null workspace");
+            a.pr[0].acc = static_cast<float*>(d_workspace);
+            a.pr[0].acc_write = 1;
+        }
+        e = make_tma_16bit(&tm[0], d_dkv, T, N, kBM, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[1], L.w.wkv, N, K, 64, false);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "project backward tensor maps");
+    if (!d_demb) tm[0] = tm[2], tm[1] = tm[3];
+    if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1];
+    e = launch_grad_products(a, tm, s);
+    if (e == cudaSuccess && a.pr[0].acc_write)
+        e = launch_sum_splits(a.pr[0].acc, a.pr[0].splits, T * K, d_demb, s);
+    if (e != cudaSuccess) return cuda_fail(e, "project backward launch");
+    return ok();
+}
+
+size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
+    if (check_loss(vocab, dim, T)) return 0;
+    Carver c(nullptr);
+    c.take<float2>((size_t)ceil_div(vocab, kBN) * 2 * T);
+    c.take<float>(T);
+    return c.at;
+}
+
+engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
+                          uint32_t vocab, uint32_t dim, const int32_t* d_labels, int64_t T,
+                          float* d_loss, float* d_lse, void* d_workspace, void* stream) {
+    engram_status st = check_loss(vocab, dim, T);
+    if (st) return st;
+    if (!ctx) return fail(ENGRAM_EINVAL, "null context");
+    if (T == 0) return ok();
+    if (!d_x || !d_head || !d_labels || !d_workspace || !aligned16(d_x) || !aligned16(d_head) ||
+        !aligned4(d_labels) || !aligned16(d_workspace) || !aligned4(d_loss) || !aligned4(d_lse))
+        return fail(ENGRAM_EINVAL, "x / head / workspace (16-byte aligned) / labels / loss / lse");
+    if ((st = train_device(ctx))) return st;
+    const cudaStream_t s = (cudaStream_t)stream;
+    Carver c(d_workspace);
+    const int n_tiles = (int)ceil_div(vocab, kBN);
+    float2* part = c.take<float2>((size_t)n_tiles * 2 * T);
+    float* zlabel = c.take<float>(T);
+    GradArgs a{};
+    a.err = ctx->d_err;
+    a.wait_limit_ns = ctx->wait_limit_ns;
+    a.pr[0] = product(T, n_tiles * (int64_t)kBN, dim, false, nullptr);
+    a.pr[0].group_m = loss_group_m(dim);
+    a.T = T;
+    a.vocab = (int)vocab;
+    a.labels = d_labels;
+    a.zlabel = zlabel;
+    a.part = part;
+    CUtensorMap tm[4];
+    cudaError_t e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
+    if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
+    if (e != cudaSuccess) return cuda_fail(e, "loss tensor maps");
+    tm[2] = tm[0], tm[3] = tm[1];
+    e = launch_grad_lse(a, tm, s);
+    if (e == cudaSuccess)
+        e = launch_loss_combine(part, n_tiles * 2, T, zlabel, d_labels, (int)vocab, d_loss, d_lse,
+                                ctx->d_err, s);
+    if (e != cudaSuccess) return cuda_fail(e, "loss launch");
+    return ok();
+}
+
+size_t engram_loss_backward_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
+    if (check_loss(vocab, dim, T) || T == 0) return 0;
+    return loss_backward_ws(nullptr, T, vocab, dim).bytes;
+}
+
+engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
+                                   uint32_t vocab, uint32_t dim, const int32_t* d_labels, int64_t T,
+                                   const float* d_lse, const float* d_dloss, uint16_t* d_dx,
+                                   uint16_t* d_dhead, void* d_workspace, void* stream) {
+    engram_status st = check_loss(vocab, dim, T);
+    if (st) return st;
+    if (!ctx) return fail(ENGRAM_EINVAL, "null context");
+    if (!aligned16(d_dx) || !aligned16(d_dhead)) return fail(ENGRAM_EINVAL, "dx / dhead (16-byte aligned)");
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (T == 0) {
+        cudaError_t e = d_dhead ? cudaMemsetAsync(d_dhead, 0, (size_t)vocab * dim * 2, s) : cudaSuccess;
+        return e == cudaSuccess ? ok() : cuda_fail(e, "loss backward of no tokens");
+    }
+    if (!d_x || !d_head || !d_labels || !d_lse || !d_dloss || !d_workspace || !aligned16(d_x) ||
+        !aligned16(d_head) || !aligned4(d_labels) || !aligned4(d_lse) || !aligned4(d_dloss) ||
+        !aligned16(d_workspace))
+        return fail(ENGRAM_EINVAL, "x / head / workspace (16-byte aligned) / labels / lse / dloss");
+    if (!d_dx && !d_dhead) return ok();
+    if ((st = train_device(ctx))) return st;
+    const LossBackWs w = loss_backward_ws(d_workspace, T, vocab, dim);
+    const int64_t step = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
+    CUtensorMap x_k, x_mn;
+    cudaError_t e = make_tma_16bit(&x_k, d_x, T, dim, kBM, false);
+    if (e == cudaSuccess) e = make_tma_16bit(&x_mn, d_x, T, dim, 64, false);
+    for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += step) {
+        const int64_t cols = std::min<int64_t>(step, vocab - v0);
+        const int64_t piece = ceil_div(cols, kBN) * kBN;
+        const bool first = v0 == 0, last = v0 + step >= vocab;
+        const uint16_t* head = d_head + v0 * dim;
+        // z of the piece, and dz from it
+        GradArgs a{};
+        a.err = ctx->d_err;
+        a.wait_limit_ns = ctx->wait_limit_ns;
+        a.pr[0] = product(T, piece, dim, false, nullptr);
+        a.pr[0].group_m = loss_group_m(dim);
+        a.T = T;
+        a.v0 = v0;
+        a.vocab = (int)vocab;
+        a.dz_chunks = (int)(piece / 64);
+        a.labels = d_labels;
+        a.lse = d_lse;
+        a.dloss = d_dloss;
+        a.dz = w.dz;
+        CUtensorMap tm[4];
+        tm[0] = tm[2] = x_k;
+        e = make_tma_16bit(&tm[1], head, vocab - v0, dim, kBM, false);
+        if (e != cudaSuccess) break;
+        tm[3] = tm[1];
+        if ((e = launch_grad_dz(a, tm, s)) != cudaSuccess) break;
+        // dx += dz head, dhead = dz^T x
+        GradArgs g{};
+        g.err = ctx->d_err;
+        g.wait_limit_ns = ctx->wait_limit_ns;
+        const uint64_t dz_rows = (uint64_t)rows * piece / 64;
+        e = make_tma_16bit(&tm[0], w.dz, dz_rows, 64, kBM, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[1], head, vocab - v0, dim, 64, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[2], w.dz, dz_rows, 64, 64, false);
+        if (e != cudaSuccess) break;
+        tm[3] = x_mn;
+        if (d_dx) {
+            g.pr[0] = loss_dx(T, dim, piece, d_dx);
+            g.pr[0].splits = std::min(w.splits, g.pr[0].kb);
+            g.pr[0].acc = w.acc;
+            g.pr[0].acc_read = !first;
+            g.pr[0].acc_write = !last || w.splits > 1;
+        }
+        if (d_dhead) g.pr[1] = loss_dhead(T, dim, cols, piece, d_dhead + v0 * dim);
+        e = launch_grad_products(g, tm, s);
+    }
+    if (e == cudaSuccess && d_dx && w.splits > 1)
+        e = launch_sum_splits(w.acc, w.splits, T * (int64_t)dim, d_dx, s);
+    if (e != cudaSuccess) return cuda_fail(e, "loss backward launch");
+    return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,575 @@
+// Matrix products of the training step on CTA pairs (tcgen05 cta_group::2,
+// TMEM accumulators, TMA operands, sm_103a):
+//
+//   loss             z = x head^T                softmax statistics as epilogue
+//   loss backward    z again, a piece of the vocabulary at a time; the epilogue
+//                    stores dz = (exp(z - lse) - [v = label]) dloss as BF16
+//                    dx += dz head (piece),  dhead (piece) = dz^T x
+//   project backward demb = dkv wkv,  dwkv = dkv^T emb
+//
+// One persistent pair per two SMs walks 256 x 256 output tiles; each CTA
+// stages its 128 rows of A and its 128 columns' half of B, 64 of the reduction
+// per stage (2 x 16 KB).  The gradient products read their operands as they lie
+// in memory: a transposed operand is loaded in boxes of 64 contiguous elements
+// x 64 reduction rows and described to the tensor core as MN-major, so nothing
+// is transposed in memory.  Two products (problems) share one launch: the long
+// one (dx, demb: few tiles, long reduction) goes first, round robin, and the
+// short one (dhead, dwkv) fills every pair up to the same number of k-blocks.
+//
+// Warp roles (320 threads): warps 0..7 epilogue, two per TMEM quadrant, each on
+// 128 of the tile's 256 columns; warp 8 TMA; warp 9 MMA issue (even CTA of the
+// pair).  Every wait is bounded as in kernels_mma.cu.
+#include <algorithm>
+#include <cmath>
+
+#include "device_common.cuh"
+#include "grad_internal.h"
+#include "tcgen05_common.cuh"
+
+namespace engram {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kOperand = kBM * kBK * 2;   // 16 KB: one CTA's A or B of a stage
+constexpr int kStage = 2 * kOperand;
+constexpr int kStages = 6;
+constexpr int kTmemCols = 2 * kBN;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kChunk = 64 * kBK * 2;      // 8 KB: 64 MN elements x 64 k of an MN-major tile
+
+constexpr int kOffBar = kStages * kStage;
+constexpr int kNumBars = 2 * kStages + 4;
+constexpr int kOffTmem = kOffBar + kNumBars * 8;
+constexpr int kOffFlag = kOffTmem + 4;
+constexpr int kSmem = kOffFlag + 4 + 1024;
+static_assert(kSmem <= 232448, "shared memory above the per-block limit");
+
+// Instruction descriptor, kind::f16, BF16 operands, fp32 accumulate, M = 256
+// (a pair), N = 256; bit 15 / 16: A / B is MN-major.
+__host__ __device__ constexpr uint32_t grad_idesc(bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(2 * kBM >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major operand in 128-byte swizzled rows of
+// 64 elements: 64-element chunks kChunk bytes apart (LBO), groups of eight k
+// 1,024 bytes apart (SBO).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kChunk >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Work item i of pair p: problem, M unit, N tile and k-block range.
+struct Item {
+    int pr, mu, nt, kb_lo, nkb, split;
+};
+
+__device__ __forceinline__ int item_count(const GradArgs& a, int p, int pairs) {
+    const int nh = a.pr[0].items > p ? (a.pr[0].items - p + pairs - 1) / pairs : 0;
+    return nh + (a.light_start[p + 1] - a.light_start[p]);
+}
+
+__device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, int i) {
+    const int nh = a.pr[0].items > p ? (a.pr[0].items - p + pairs - 1) / pairs : 0;
+    Item it;
+    int idx;
+    if (i < nh) {
+        it.pr = 0;
+        idx = p + i * pairs;
+    } else {
+        it.pr = 1;
+        idx = a.light_start[p] + (i - nh);
+    }
+    const GradProblem& q = a.pr[it.pr];
+    const int tiles = q.m_units * q.n_tiles;
+    it.split = idx / tiles;
+    idx -= it.split * tiles;
+    if (q.n_fast) {
+        it.mu = idx / q.n_tiles;
+        it.nt = idx - it.mu * q.n_tiles;
+    } else {  // groups of group_m units, M inner: the pairs in flight share B tiles in L2
+        const int per = q.group_m * q.n_tiles;
+        const int g = idx / per, first = g * q.group_m;
+        const int gm = min(q.group_m, q.m_units - first);
+        const int r = idx - g * per;
+        it.nt = r / gm;
+        it.mu = first + (r - it.nt * gm);
+    }
+    it.kb_lo = (int)((int64_t)it.split * q.kb / q.splits);
+    it.nkb = (int)((int64_t)(it.split + 1) * q.kb / q.splits) - it.kb_lo;
+    return it;
+}
+
+// kEpi: what becomes of a tile.  kBMn: B is MN-major (the gradient products).
+template <int kEpi, bool kBMn>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+       const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+       const __grid_constant__ GradArgs a) {
+    const uint32_t rank = cluster_ctarank();
+    const bool issuer = rank == 0u;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto full = [&](int s) { return sbase + kOffBar + 8u * (uint32_t)s; };
+    auto empty = [&](int s) { return sbase + kOffBar + 8u * (uint32_t)(kStages + s); };
+    auto tfull = [&](int acc) { return sbase + kOffBar + 8u * (uint32_t)(2 * kStages + acc); };
+    auto tempty = [&](int acc) { return sbase + kOffBar + 8u * (uint32_t)(2 * kStages + 2 + acc); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffFlag);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1u);
+            mbar_init(empty(s), 1u);
+        }
+        for (int acc = 0; acc < 2; ++acc) {
+            mbar_init(tfull(acc), 1u);
+            mbar_init(tempty(acc), 2u * kEpiWarps);  // the epilogue warps of both CTAs
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWarpMma) tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int n_items = item_count(a, pair, pairs);
+    const long long lim = a.wait_limit_ns;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(a.err, kErrTimeout);
+    };
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; i < n_items && ok; ++i) {
+                const Item w = get_item(a, pair, pairs, i);
+                const GradProblem& q = a.pr[w.pr];
+                const CUtensorMap* tmA = w.pr ? &tmA1 : &tmA0;
+                const CUtensorMap* tmB = w.pr ? &tmB1 : &tmB0;
+                const int mb = 2 * w.mu + (int)rank;               // this CTA's 128 rows of A
+                const int n0 = w.nt * kBN + (int)rank * (kBN / 2);  // and its half of B
+                for (int j = 0; j < w.nkb; ++j, ++it) {
+                    const int s = it % kStages;
+                    const int kb = w.kb_lo + j;
+                    if (!mbar_wait(empty(s), ((uint32_t)(it / kStages) & 1u) ^ 1u, abort_flag, lim)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    if (issuer) mbar_expect_tx(full(s), 2 * kStage);
+                    const uint32_t bar = map_rank(full(s), 0);
+                    const uint32_t sa = sbase + (uint32_t)(s * kStage), sb = sa + kOperand;
+                    if (q.a_mn) {
+                        if (q.a_tiled) {  // 128 x 64 tiles [reduction block][M chunk]
+                            const int y = ((kb >> 1) * q.a_tiled + 2 * mb) * 128 + (kb & 1) * 64;
+                            tma_load_2d_pair(sa, tmA, bar, 0, y);
+                            tma_load_2d_pair(sa + kChunk, tmA, bar, 0, y + 128);
+                        } else {
+                            tma_load_2d_pair(sa, tmA, bar, mb * kBM, kb * kBK);
+                            tma_load_2d_pair(sa + kChunk, tmA, bar, mb * kBM + 64, kb * kBK);
+                        }
+                    } else if (q.a_tiled) {  // 128 x 64 tiles [M block][reduction chunk]
+                        tma_load_2d_pair(sa, tmA, bar, 0, (mb * q.a_tiled + kb) * 128);
+                    } else {
+                        tma_load_2d_pair(sa, tmA, bar, kb * kBK, mb * kBM);
+                    }
+                    if (kBMn) {
+                        tma_load_2d_pair(sb, tmB, bar, n0, kb * kBK);
+                        tma_load_2d_pair(sb + kChunk, tmB, bar, n0 + 64, kb * kBK);
+                    } else {
+                        tma_load_2d_pair(sb, tmB, bar, kb * kBK, n0);
+                    }
+                }
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0 && issuer) {
+            int it = 0;
+            bool ok = true;
+            for (int i = 0; i < n_items && ok; ++i) {
+                const int acc = i & 1;
+                if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag, lim)) {
+                    fail();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
+                const Item w = get_item(a, pair, pairs, i);
+                const bool a_mn = a.pr[w.pr].a_mn != 0;
+                const uint32_t id = grad_idesc(a_mn, kBMn);
+                // 16 of the reduction: 32 bytes of a K-major row, or 16 rows of 128 bytes
+                const uint64_t a_step = a_mn ? 128ull : 2ull, b_step = kBMn ? 128ull : 2ull;
+                for (int j = 0; j < w.nkb; ++j, ++it) {
+                    const int s = it % kStages;
+                    if (!mbar_wait_cluster(full(s), (uint32_t)(it / kStages) & 1u, abort_flag, lim)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = sbase + (uint32_t)(s * kStage), sb = sa + kOperand;
+                    const uint64_t ad = a_mn ? sdesc_mn(sa) : sdesc_sw128(sa);
+                    const uint64_t bd = kBMn ? sdesc_mn(sb) : sdesc_sw128(sb);
+#pragma unroll
+                    for (int k = 0; k < kBK / 16; ++k)
+                        umma_f16kind_pair(d_tmem, ad + a_step * k, bd + b_step * k, id,
+                                          (j != 0) || (k != 0));
+                    umma_commit_pair(empty(s));
+                }
+                if (ok) umma_commit_pair(tfull(acc));
+            }
+        }
+    } else {
+        // ---- epilogue ----
+        const int q4 = warp & 3, grp = warp >> 2;  // TMEM quadrant; columns [128 grp, 128 grp + 128)
+        const int m = q4 * 32 + lane;
+        for (int i = 0; i < n_items; ++i) {
+            const Item w = get_item(a, pair, pairs, i);
+            const GradProblem& q = a.pr[w.pr];
+            const int acc = i & 1;
+            const int64_t row = ((int64_t)2 * w.mu + rank) * kBM + m;
+            const int col0 = w.nt * kBN + grp * 128;
+            const uint32_t taddr = tmem_base + (uint32_t)(acc * kBN + grp * 128) +
+                                   ((uint32_t)(q4 * 32) << 16);
+            float lse = 0.f, dl = 0.f;
+            int label = -1;
+            if (kEpi == kGradLse || kEpi == kGradDz) {
+                if (row < a.T) {
+                    label = a.labels[row];
+                    if (label >= a.vocab) label = -1;
+                    if (kEpi == kGradDz) {
+                        lse = a.lse[row];
+                        dl = label >= 0 ? a.dloss[row] : 0.f;
+                    }
+                }
+            }
+            int ready = 1;
+            if (lane == 0) ready = mbar_wait_cluster(tfull(acc), (uint32_t)(i >> 1) & 1u, abort_flag, lim);
+            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            if (!ready) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            if constexpr (kEpi == kGradLse) {
+                // running maximum and sum over this warp's 128 columns
+                float mx = -INFINITY, sum = 0.f;
+                const int64_t zrel = (int64_t)label - col0;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    __syncwarp();
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+                    tmem_wait_ld();
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    if (label >= 0 && zrel >= c * 32 && zrel < c * 32 + 32) {
+                        float z = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (zrel == c * 32 + j) z = v[j];
+                        a.zlabel[row] = z;
+                    }
+                    const int lastc = a.vocab - (col0 + c * 32);
+                    if (lastc < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= lastc) v[j] = -INFINITY;
+                    }
+                    float cm = v[0];
+                    bool nan = v[0] != v[0];
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) {
+                        nan |= v[j] != v[j];
+                        cm = fmaxf(cm, v[j]);
+                    }
+                    const float nm = fmaxf(mx, cm);
+                    const float base = nm == -INFINITY ? 0.f : nm;
+                    float cs = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) cs += exp2f((v[j] - base) * kLog2e);
+                    sum = sum * exp2f((mx - base) * kLog2e) + cs;
+                    if (nan) sum = NAN;
+                    mx = nm;
+                }
+                if (row < a.T)
+                    a.part[((int64_t)w.nt * 2 + grp) * a.T + row] = make_float2(mx, sum);
+            } else if constexpr (kEpi == kGradDz) {
+                // columns of this warp: two 64-wide chunks of the tiled dz
+                const int64_t tb = 2 * w.mu + rank;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    __syncwarp();
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+                    tmem_wait_ld();
+                    const int lc = col0 + c * 32;           // column within the piece
+                    const int64_t v0 = a.v0 + lc;            // column within the vocabulary
+                    const int64_t rel = (int64_t)label - v0;
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float d[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            // (z - lse first: exact where p is near 1)
+                            float p = exp2f((__uint_as_float(r[j + u]) - lse) * kLog2e);
+                            if (rel == j + u) p -= 1.f;
+                            d[u] = label >= 0 && v0 + j + u < a.vocab ? p * dl : 0.f;
+                        }
+                        o[j / 2] = bf16x2_pack_rn(d[0], d[1]);
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        a.dz + ((tb * a.dz_chunks + (lc >> 6)) * 128 + m) * 64 + (lc & 63));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+            } else {
+                // a product's output: BF16, from this reduction alone or added to
+                // what earlier pieces left in fp32; or the fp32 sum of a split
+                const bool in = row < q.M;
+                float* accp = q.acc ? q.acc + ((int64_t)w.split * q.M + row) * q.N : nullptr;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    __syncwarp();
+                    uint32_t r[32];
+                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
+                    tmem_wait_ld();
+                    const int64_t n = col0 + c * 32;
+                    if (!in) continue;
+                    // N is a multiple of 8: groups of eight columns are in or out whole
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (n + j >= q.N) continue;
+                        float v[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(r[j + u]);
+                        if (q.acc_read) {
+                            const float4 x = *reinterpret_cast<const float4*>(accp + n + j);
+                            const float4 y = *reinterpret_cast<const float4*>(accp + n + j + 4);
+                            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+                        }
+                        if (q.acc_write) {
+                            *reinterpret_cast<float4*>(accp + n + j) = make_float4(v[0], v[1], v[2], v[3]);
+                            *reinterpret_cast<float4*>(accp + n + j + 4) =
+                                make_float4(v[4], v[5], v[6], v[7]);
+                        } else {
+                            *reinterpret_cast<uint4*>(q.out + row * q.N + n + j) =
+                                make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
+                                           bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(tempty(acc), 0));
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag) {
+        // let copies and MMAs still in flight land before TMEM is freed
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+        __syncthreads();
+    }
+    cluster_sync();  // no arrival or multicast may target a CTA that exited
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+// loss and lse of each row from the column groups' (maximum, sum) pairs, in
+// column order within each of the block's eight slices of the groups, then the
+// slices in order.
+__global__ void k_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,
+                               const int32_t* labels, int vocab, float* loss, float* lse,
+                               uint32_t* err) {
+    pdl_wait();
+    __shared__ float2 sm[8][32];
+    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+    float mx = -INFINITY, sum = 0.f;
+    if (t < T) {
+        const int lo = sl * groups / 8, hi = (sl + 1) * groups / 8;
+        for (int g = lo; g < hi; ++g) {
+            const float2 p = part[(int64_t)g * T + t];
+            const float nm = fmaxf(mx, p.x);
+            const float b = nm == -INFINITY ? 0.f : nm;
+            sum = sum * expf(mx - b) + p.y * expf(p.x - b);
+            mx = nm;
+        }
+    }
+    sm[sl][lane] = make_float2(mx, sum);
+    __syncthreads();
+    if (sl || t >= T) return;
+    for (int k = 1; k < 8; ++k) {
+        const float2 p = sm[k][lane];
+        const float nm = fmaxf(mx, p.x);
+        const float b = nm == -INFINITY ? 0.f : nm;
+        sum = sum * expf(mx - b) + p.y * expf(p.x - b);
+        mx = nm;
+    }
+    const float l = mx + logf(sum);
+    const int y = labels[t];
+    if (y >= vocab) atomicOr(err, kErrBounds);
+    if (lse) lse[t] = l;
+    if (loss) loss[t] = y >= 0 && y < vocab ? l - zlabel[t] : 0.f;
+}
+
+// out = the sum of the splits' fp32 buffers, in order, rounded to BF16 (n a
+// multiple of 8).
+__global__ void k_sum_splits(const float* acc, int splits, int64_t n, uint16_t* out) {
+    pdl_wait();
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    if (i >= n) return;
+    float v[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4 x = *reinterpret_cast<const float4*>(acc + s * n + i);
+        const float4 y = *reinterpret_cast<const float4*>(acc + s * n + i + 4);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    *reinterpret_cast<uint4*>(out + i) =
+        make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
+                   bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
+}
+
+// The pairs' shares of the short problem: pair p has the k-blocks of its round-
+// robin items of the long one; each is filled up to the common mean.
+void share_items(GradArgs& a, int pairs) {
+    auto cost = [](const GradProblem& q) { return q.items ? (double)q.kb / q.splits + 1.0 : 0.0; };
+    const double ch = cost(a.pr[0]), cl = cost(a.pr[1]);
+    const int H = a.pr[0].items, L = a.pr[1].items;
+    const double mean = (H * ch + L * cl) / pairs;
+    double want = 0;  // items the pairs so far should have taken
+    double total = 0;
+    auto room = [&](int p) {
+        const int nh = H > p ? (H - p + pairs - 1) / pairs : 0;
+        return std::max(0.0, mean - nh * ch);
+    };
+    for (int p = 0; p < pairs; ++p) total += room(p);
+    a.light_start[0] = 0;
+    for (int p = 0; p < pairs; ++p) {
+        want += total > 0 ? room(p) / total * L : (double)L / pairs;
+        a.light_start[p + 1] = p + 1 == pairs ? L : std::min(L, (int)std::floor(want + 0.5));
+    }
+}
+
+cudaError_t pdl_launch(void* f, dim3 grid, dim3 block, void** args, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, f, args);
+}
+
+// CTA pairs that are resident at once: a launch has no more, since its items are
+// dealt out for pairs that all run from the start.
+template <int kEpi, bool kBMn>
+cudaError_t resident_pairs(int* pairs) {
+    static int known = 0;
+    if (!known) {
+        auto kern = k_grad<kEpi, kBMn>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * (device_sm_count() / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        known = std::min(std::min(n, device_sm_count() / 2), kMaxPairs);
+    }
+    *pairs = known;
+    return cudaSuccess;
+}
+
+template <int kEpi, bool kBMn>
+cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
+    auto kern = k_grad<kEpi, kBMn>;
+    for (GradProblem& q : a.pr) q.items = q.m_units * q.n_tiles * q.splits;
+    const int total = a.pr[0].items + a.pr[1].items;
+    if (!total) return cudaSuccess;
+    int pairs = 0;
+    cudaError_t e = resident_pairs<kEpi, kBMn>(&pairs);
+    if (e != cudaSuccess) return e;
+    pairs = std::min(pairs, total);
+    share_items(a, pairs);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], a);
+}
+
+}  // namespace
+
+int grad_pairs() { return std::min(device_sm_count() / 2, kMaxPairs); }
+
+cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
+    return launch<kGradLse, false>(a, tm, s);
+}
+cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
+    return launch<kGradDz, false>(a, tm, s);
+}
+cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
+    return launch<kGradOut, true>(a, tm, s);
+}
+
+cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,
+                                const int32_t* labels, int vocab, float* loss, float* lse,
+                                uint32_t* err, cudaStream_t s) {
+    void* args[] = {&part, &groups, &T, &zlabel, &labels, &vocab, &loss, &lse, &err};
+    return pdl_launch((void*)k_loss_combine, dim3((unsigned)((T + 31) / 32)), dim3(256), args, s);
+}
+
+cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, uint16_t* out,
+                              cudaStream_t s) {
+    void* args[] = {&acc, &splits, &n, &out};
+    return pdl_launch((void*)k_sum_splits, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), args, s);
+}
+
+}  // namespace engram

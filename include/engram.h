@@ -451,6 +451,129 @@ engram_status engram_gate_bf16kv(const engram_ctx* ctx, int layer, const uint16_
                                  const uint32_t* d_windows, int64_t T, uint16_t* d_hidden,
                                  float* d_gates, void* stream);
 
+/* ---- training -------------------------------------------------------------------
+ * The backward pass of the step, and the two ends of a model that holds such
+ * layers (the pages train them: FlagScale plugin, section 5).  Together:
+ * engram_embed writes the token embeddings into the branches; engram_prepass and
+ * engram_gate_checkpoint run the layer and keep its activations in 8 bits;
+ * engram_loss and engram_loss_backward end the forward pass and begin the
+ * backward one; engram_gate_backward_checkpoint and engram_project_backward take
+ * the gradient to the norm weights, wkv and the gathered rows; engram_embed_grad
+ * sums it over equal ids, for the token embedding and for the n-gram table alike.
+ * Gradients are BF16 where the value they belong to is (each rounded once, from
+ * an fp32 sum), fp32 for w_q, w_k and the embeddings' rows.  Results do not
+ * depend on the order in which blocks run.  A context with no bound layer gets
+ * its 16-byte device word at its first engram_embed, engram_embed_grad,
+ * engram_loss or engram_loss_backward: make that call before a stream capture.
+ * Workspaces are device memory, 16-byte aligned, free again when the call's work
+ * on the stream is done. */
+
+/* Embedding lookup with scaling: out[t][c] = scale table[ids[t]] for c < copies
+ * (the hyper-connection branches start as copies of one embedding).
+ * d_table [rows][dim], fp32 or BF16; d_ids uint32 [n]; d_out bf16
+ * [n][copies][dim], rounded once.  ENGRAM_MASKED gives zeros; any other id >=
+ * rows gives zeros and sets the error word (ENGRAM_EBOUNDS at the next
+ * engram_sync).  dim: a multiple of 8 up to 65,536; copies 1..8; rows up to
+ * 2^32 - 2; n up to 2^30.  d_table and d_out 16-byte aligned. */
+#define ENGRAM_EMBED_F32 0
+#define ENGRAM_EMBED_BF16 1
+engram_status engram_embed(engram_ctx* ctx, const void* d_table, int table_format, uint64_t rows,
+                           uint32_t dim, const uint32_t* d_ids, int64_t n, float scale,
+                           uint32_t copies, uint16_t* d_out, void* stream);
+/* Its gradient by sorted ids: the row of id v is scale times the sum of dout[t][c]
+ * (bf16 [n][copies][dim]) over the t with ids[t] == v and every c, in fp32.
+ * Masked ids and ids >= rows take no part (the latter set the error word).
+ *  sparse (d_unique given): d_unique uint32 [n] gets the distinct ids in
+ *    ascending order, d_count uint32 their number, d_grad fp32 [n][dim] one row
+ *    for each; entries past the count are not written.  accumulate must be 0.
+ *    The gradient of an n-gram table, whose ids are engram_hash's rows [T][nb]
+ *    (n = T nb, dim = row_dim, copies 1, dout = demb [T][K]).
+ *  dense (d_unique NULL, d_count may be): d_grad fp32 [rows][dim]; with
+ *    accumulate 0 it is written whole, with 1 the sums are added to it.
+ * d_workspace: engram_embed_grad_workspace_bytes(n, rows, dim) bytes. */
+size_t engram_embed_grad_workspace_bytes(int64_t n, uint64_t rows, uint32_t dim);
+engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, const uint32_t* d_ids,
+                                int64_t n, float scale, uint32_t copies, const uint16_t* d_dout,
+                                uint32_t* d_unique, uint32_t* d_count, float* d_grad,
+                                int accumulate, void* d_workspace, void* stream);
+
+/* The gate (as engram_gate, "第三步"), with what its backward pass needs kept in
+ * 8 bits: per token the hidden state before the step, the keys and the value,
+ * (2 hc + 1) d values in that order as MXFP8 (E4M3 codes, one E8M0 exponent per
+ * 32 values: the smallest that keeps the block's largest magnitude at or below
+ * 448; codes rounded to nearest even; a block that holds an infinity or NaN
+ * decodes to NaN) - 47,520 bytes at hc 4, d 5,120, against 92,160 of BF16.
+ * d_kv [T][N] fp32 or BF16 (kv_format, as engram_prepass); d_hidden bf16
+ * [T][hc][d], read; d_hidden_out, written, may be d_hidden; d_gates fp32
+ * [T][hc] or NULL; d_codes uint8 [T][(2 hc + 1) d]; d_scales uint8
+ * [T][(2 hc + 1) d / 32].  An image row passes through, its kv is not read
+ * and its checkpoint is zero.  All 16-byte aligned. */
+engram_status engram_gate_checkpoint(const engram_ctx* ctx, int layer, const void* d_kv,
+                                     int kv_format, const uint32_t* d_windows, int64_t T,
+                                     const uint16_t* d_hidden, uint16_t* d_hidden_out,
+                                     float* d_gates, uint8_t* d_codes, uint8_t* d_scales,
+                                     void* stream);
+/* The gate's backward pass.  From dout (bf16 [T][hc][d], the gradient of the
+ * updated hidden state) and the activations: dhidden bf16 [T][hc][d] (may be
+ * dout), dkv bf16 [T][N], and dwq, dwk fp32 [hc][d] summed over the tokens
+ * (each may be NULL; written, not added to).  With x the dot product of the
+ * gate, s = copysign(sqrt(max(|x|, 1e-6)), x) and g = sigmoid(s):
+ *   dx = (sum_i dout_i v_i) g (1 - g) / (2 |s|)  where |x| > 1e-6, else 0,
+ * and from it the gradients of the two RMS norms and the dot product; dv =
+ * sum_b g_b dout_b.  An image row passes dout through and has no dkv.
+ * engram_gate_backward takes the hidden state before the step and kv as they
+ * were, engram_gate_backward_checkpoint the 8-bit checkpoint of
+ * engram_gate_checkpoint: the gradient at the values that the checkpoint holds.
+ * d_workspace: engram_gate_backward_workspace_bytes(ctx, T) bytes. */
+size_t engram_gate_backward_workspace_bytes(const engram_ctx* ctx, int64_t T);
+engram_status engram_gate_backward(const engram_ctx* ctx, int layer, const void* d_kv,
+                                   int kv_format, const uint16_t* d_hidden,
+                                   const uint32_t* d_windows, int64_t T, const uint16_t* d_dout,
+                                   uint16_t* d_dhidden, uint16_t* d_dkv, float* d_dwq, float* d_dwk,
+                                   void* d_workspace, void* stream);
+engram_status engram_gate_backward_checkpoint(const engram_ctx* ctx, int layer,
+                                              const uint8_t* d_codes, const uint8_t* d_scales,
+                                              const uint32_t* d_windows, int64_t T,
+                                              const uint16_t* d_dout, uint16_t* d_dhidden,
+                                              uint16_t* d_dkv, float* d_dwq, float* d_dwk,
+                                              void* d_workspace, void* stream);
+
+/* The projection's backward pass: demb = dkv wkv (bf16 [T][K]) and dwkv =
+ * dkv^T emb (bf16 [N][K], the sum over the tokens), from dkv bf16 [T][N] and
+ * the dequantised rows emb bf16 [T][K] (engram_gather_dequant).  demb or dwkv
+ * may be NULL (without dwkv, d_emb may be too).  Products in BF16, sums in fp32.
+ * d_workspace: engram_project_backward_workspace_bytes(ctx, T) bytes (may be 0,
+ * then NULL will do). */
+size_t engram_project_backward_workspace_bytes(const engram_ctx* ctx, int64_t T);
+engram_status engram_project_backward(const engram_ctx* ctx, int layer, const uint16_t* d_emb,
+                                      const uint16_t* d_dkv, int64_t T, uint16_t* d_demb,
+                                      uint16_t* d_dwkv, void* d_workspace, void* stream);
+
+/* Softmax cross entropy of z = x head^T over a large vocabulary, the logits
+ * never stored: lse[t] = log sum_v exp(z_tv), loss[t] = lse[t] - z_t,label
+ * (fp32 [T], each may be NULL).  d_x bf16 [T][dim]; d_head bf16 [vocab][dim];
+ * d_labels int32 [T]: a negative label is ignored (loss 0), one >= vocab is
+ * too and sets the error word (ENGRAM_EBOUNDS).  dim: a multiple of 8 up to
+ * 65,536; any vocab.  d_x, d_head 16-byte aligned.
+ * d_workspace: engram_loss_workspace_bytes(T, vocab, dim) bytes. */
+size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim);
+engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
+                          uint32_t vocab, uint32_t dim, const int32_t* d_labels, int64_t T,
+                          float* d_loss, float* d_lse, void* d_workspace, void* stream);
+/* Its gradient, in pieces of the vocabulary: the logits of a piece are computed
+ * again, dz = (exp(z - lse) - [v = label]) dloss[t] (0 where the label is
+ * ignored) is kept as BF16 for that piece only, and dx = dz head (bf16
+ * [T][dim]) and dhead = dz^T x (bf16 [vocab][dim], written) are summed in fp32
+ * and rounded once.  d_lse: engram_loss's; d_dloss fp32 [T]; d_dx or d_dhead
+ * may be NULL.  d_workspace: engram_loss_backward_workspace_bytes(T, vocab, dim)
+ * bytes: the piece's dz (about 64 MB, 8 KB per token for a very long batch)
+ * and the fp32 dx. */
+size_t engram_loss_backward_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim);
+engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
+                                   uint32_t vocab, uint32_t dim, const int32_t* d_labels, int64_t T,
+                                   const float* d_lse, const float* d_dloss, uint16_t* d_dx,
+                                   uint16_t* d_dhead, void* d_workspace, void* stream);
+
 /* Synchronise `stream`, then read and clear the context's device error word:
  * ENGRAM_EBOUNDS / ENGRAM_ETIMEOUT if a kernel reported one, ENGRAM_ECUDA on
  * an asynchronous CUDA error. */

@@ -1,0 +1,93 @@
+"""Refusals of the training operators (no GPU): arguments are checked before any launch."""
+import numpy as np
+import pytest
+
+import engram_gram_conditional_gb300 as eg
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from engram_gram_conditional_gb300 import build
+
+    build.build()
+    c = eg.engram_ctx_create(64, 60, np.arange(64, dtype=np.uint32) % 60, [3], [50], heads=2,
+                             row_dim=32, hc=2, d=256)
+    yield c
+    eg.engram_ctx_destroy(c)
+
+
+A = 1 << 20  # an aligned address that no refused call touches
+
+
+def refused(status, f, *args):
+    with pytest.raises(eg.EngramError) as e:
+        f(*args)
+    assert e.value.status == status
+
+
+EMBED = dict(table=A, fmt=eg.EMBED_BF16, rows=10, dim=64, ids=A, n=4, scale=1.0, copies=1, out=A)
+
+
+@pytest.mark.parametrize("bad", [dict(table=None), dict(ids=None), dict(out=None), dict(table=A + 8),
+                                 dict(out=A + 2), dict(ids=A + 1), dict(fmt=2), dict(fmt=-1),
+                                 dict(rows=0), dict(rows=2**32 - 1), dict(dim=0), dict(dim=12),
+                                 dict(dim=65544), dict(n=-1), dict(n=2**30 + 1), dict(copies=0),
+                                 dict(copies=9)])
+def test_embed_refuses(ctx, bad):
+    a = {**EMBED, **bad}
+    refused(eg.EINVAL, eg.engram_embed, ctx, a["table"], a["fmt"], a["rows"], a["dim"], a["ids"],
+            a["n"], a["scale"], a["copies"], a["out"])
+    refused(eg.EINVAL, eg.engram_embed, None, *list(EMBED.values()))
+
+
+GRAD = dict(rows=10, dim=64, ids=A, n=4, scale=1.0, copies=1, dout=A, unique=A, count=A, grad=A,
+            accumulate=0, ws=A)
+
+
+@pytest.mark.parametrize("bad", [dict(ids=None), dict(dout=None), dict(grad=None), dict(ws=None),
+                                 dict(count=None), dict(accumulate=1), dict(accumulate=2),
+                                 dict(dout=A + 4), dict(grad=A + 4), dict(ws=A + 4),
+                                 dict(unique=A + 1), dict(dim=4), dict(copies=0), dict(n=-1)])
+def test_embed_grad_refuses(ctx, bad):
+    refused(eg.EINVAL, eg.engram_embed_grad, ctx, *{**GRAD, **bad}.values())
+
+
+LOSS = dict(x=A, head=A, vocab=100, dim=64, labels=A, T=4, loss=A, lse=A, ws=A)
+
+
+@pytest.mark.parametrize("bad", [dict(x=None), dict(head=None), dict(labels=None), dict(ws=None),
+                                 dict(x=A + 8), dict(head=A + 8), dict(ws=A + 8), dict(vocab=0),
+                                 dict(dim=0), dict(dim=20), dict(T=-1), dict(T=2**24 + 1)])
+def test_loss_refuses(ctx, bad):
+    refused(eg.EINVAL, eg.engram_loss, ctx, *{**LOSS, **bad}.values())
+
+
+BACK = dict(x=A, head=A, vocab=100, dim=64, labels=A, T=4, lse=A, dloss=A, dx=A, dhead=A, ws=A)
+
+
+@pytest.mark.parametrize("bad", [dict(x=None), dict(lse=None), dict(dloss=None), dict(ws=None),
+                                 dict(dx=A + 8), dict(dhead=A + 8), dict(vocab=2**30 + 1),
+                                 dict(dim=7), dict(T=-1)])
+def test_loss_backward_refuses(ctx, bad):
+    refused(eg.EINVAL, eg.engram_loss_backward, ctx, *{**BACK, **bad}.values())
+
+
+def test_layer_operators_need_a_bound_layer(ctx):
+    refused(eg.ESTATE, eg.engram_gate_checkpoint, ctx, 0, A, eg.KV_F32, A, 1, A, A, None, A, A)
+    refused(eg.ESTATE, eg.engram_gate_backward, ctx, 0, A, eg.KV_F32, A, A, 1, A, A, A, A, A, A)
+    refused(eg.ESTATE, eg.engram_gate_backward_checkpoint, ctx, 0, A, A, A, 1, A, A, A, A, A, A)
+    refused(eg.ESTATE, eg.engram_project_backward, ctx, 0, A, A, 1, A, A, A)
+    refused(eg.EINVAL, eg.engram_gate_checkpoint, ctx, 1, A, eg.KV_F32, A, 1, A, A, None, A, A)
+    refused(eg.EINVAL, eg.engram_project_backward, None, 0, A, A, 1, A, A, A)
+
+
+def test_workspace_sizes(ctx):
+    assert eg.engram_embed_grad_workspace_bytes(0, 10, 64) > 0
+    assert eg.engram_embed_grad_workspace_bytes(4, 10, 12) == 0
+    assert eg.engram_gate_backward_workspace_bytes(ctx, -1) == 0
+    assert eg.engram_project_backward_workspace_bytes(ctx, 0) == 0
+    assert eg.engram_loss_workspace_bytes(4, 0, 64) == 0
+    assert eg.engram_loss_backward_workspace_bytes(0, 100, 64) == 0
+    # no logits: the loss keeps two floats per 128 columns, the backward pass one piece
+    assert eg.engram_loss_workspace_bytes(2048, 129_280, 5120) < 2048 * 129_280 // 8
+    assert eg.engram_loss_backward_workspace_bytes(2048, 129_280, 5120) < 2048 * 129_280 * 2 // 4
