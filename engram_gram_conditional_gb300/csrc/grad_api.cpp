@@ -93,6 +93,8 @@ GateTrain gate_args(const engram_ctx* ctx, int layer, const uint32_t* windows, i
     a.wqk = L.wqk;
     a.wq = L.w.wq;
     a.wk = L.w.wk;
+    a.err = ctx->d_err;
+    a.wait_limit_ns = ctx->wait_limit_ns;
     return a;
 }
 

@@ -118,6 +118,8 @@ struct GateTrain {
     float *dwq, *dwk;
     float4* factors;         // [T][hc]
     float* dw_part;          // [gate_backward_shares][hc][d]
+    uint32_t* err;
+    long long wait_limit_ns;
 };
 cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t s);
 int gate_backward_shares(int64_t T, int d);

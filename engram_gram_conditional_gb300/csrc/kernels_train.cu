@@ -628,11 +628,455 @@ __device__ __forceinline__ float4 gate_factors(float skk, float shh, float s, fl
     const float rs = rh * rk / sqrtf((float)d);
     const float x = rs * s;
     const float root = sqrtf(fmaxf(fabsf(x), 1e-6f));
-    const float g = 1.0f / (1.0f + expf(-copysignf(root, x)));
-    const float dx = fabsf(x) > 1e-6f ? dyv * g * (1.0f - g) / (2.0f * root) : 0.f;
+    // g (1 - g) = e / (1 + e)^2 with e = exp(-|s|): 1 - g itself would lose a
+    // saturated gate's slope to cancellation
+    const float e = expf(-root);
+    const float g = (signbit(x) ? e : 1.0f) / (1.0f + e);
+    const float dx = fabsf(x) > 1e-6f ? dyv * e / ((1.0f + e) * (1.0f + e) * 2.0f * root) : 0.f;
     return make_float4(dx * rs, dx * x * rh * rh * inv_d, dx * x * rk * rk * inv_d, g);
 }
 
+// ---- fused: one pass over a token's activations --------------------------------------------
+// A cluster of CTAs takes one token at a time, each CTA a range of its columns:
+// bulk copies bring the range of every row (hidden, keys, value, dout) into a
+// ring of stages; phase 1 sums over the columns, the CTAs exchange 4 sums per
+// branch through distributed shared memory, and phase 2 reads the stage again
+// for the outputs, so each byte comes from HBM once.  Phase 2 of token i - 1
+// runs after phase 1 of token i, which hides the exchange.  A thread of the
+// compute warps owns 8 columns of every branch: its norm weights and its share
+// of their gradient stay in registers over all tokens of the cluster.  Two more
+// warps: one loads, one adds the warps' sums, exchanges them and turns them into
+// the factors, so that the compute warps wait for data and factors only.
+// What bounds it beside HBM is the issue rate, so the arithmetic runs on pairs of
+// values (f32x2), and an 8-bit block's scale multiplies the sums and factors
+// instead of its values.
+constexpr int kFusedMaxWarps = 10;  // compute warps
+constexpr int kFusedSlots = 4;      // tokens between phase 1 and phase 2 at most 2
+constexpr int kFusedMaxStages = 8;
+constexpr int kFusedFixed =
+    kFusedSlots * (kFusedMaxWarps * 32 + 8 * 32 + 32) * 4 + (2 * kFusedMaxStages + 3 * kFusedSlots) * 8 + 128;
+static_assert(kFusedFixed % 16 == 0, "");
+
+template <int kSaved>
+__host__ __device__ constexpr int fused_row_bytes(int hc) {  // of all rows, per column
+    return kSaved == kSavedMx ? (2 * hc + 1) + 2 * hc
+                              : 2 * hc + (hc + 1) * (kSaved == kSavedF32 ? 4 : 2) + 2 * hc;
+}
+template <int kSaved>
+__host__ __device__ constexpr int fused_stage_bytes(int hc, int cols) {
+    return (fused_row_bytes<kSaved>(hc) * cols + (kSaved == kSavedMx ? (2 * hc + 1) * cols / 32 : 0) +
+            127) / 128 * 128;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// Pairs of fp32 values.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float both(f32x2 v) {
+    const float2 f = unpair(v);
+    return f.x + f.y;
+}
+__device__ __forceinline__ void unpack8(uint4 v, f32x2 (&f)[4]) {
+    f[0] = pair(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = pair(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = pair(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = pair(bf16_lo(v.w), bf16_hi(v.w));
+}
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+    const float2 f = unpair(v);
+    return bf16x2_pack_rn(f.x, f.y);
+}
+__device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
+    return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+// Eight E4M3 codes without their block's scale.
+__device__ __forceinline__ void decode8(uint2 w, f32x2 (&f)[4]) {
+    const uint32_t h[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t x;
+        asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(x)
+            : "r"(h[j]));
+        const float2 v = __half22float2(*reinterpret_cast<__half2*>(&x));
+        f[j] = pair(v.x, v.y);
+    }
+}
+
+// Sums over the warp of kN values (a power of two, at most 32), each exchange
+// halving what a lane still holds; lane l ends with value l / (32 / kN).
+template <int kN>
+__device__ __forceinline__ float warp_sums(float (&v)[kN], int lane) {
+#pragma unroll
+    for (int k = 0; (kN >> k) > 1; ++k) {
+        const int o = 16 >> k, half = kN >> (k + 1);
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+            const float send = up ? v[j] : v[j + half];
+            const float keep = up ? v[j + half] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+    }
+#pragma unroll
+    for (int o = 16 / kN; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    return v[0];
+}
+
+// kExact: hc == kHc (no branch is left out).
+template <int kSaved, int kHc, bool kExact>
+__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
+k_gate_backward_fused(const GateTrain a, int stages, int cs) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kSums = 4 * kHc;
+    const int hc = kExact ? kHc : a.hc;
+    const int d = a.d;
+    const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
+    const int groups = d / 256;  // 256 columns: a warp's
+    const int g0 = groups * rank / cs, warps = groups * (rank + 1) / cs - g0;
+    const int max_cols = ((groups + cs - 1) / cs) * 256;
+    const int cols = warps * 256, col0 = g0 * 256;
+    const int stage_bytes = fused_stage_bytes<kSaved>(hc, max_cols);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int loader = (int)(blockDim.x >> 5) - 2, joiner = loader + 1;
+
+    float* wred = reinterpret_cast<float*>(smem);            // [slots][warps][32]
+    float* red = wred + kFusedSlots * kFusedMaxWarps * 32;   // [slots][8 ranks][32]
+    float4* fac = reinterpret_cast<float4*>(red + kFusedSlots * 8 * 32);  // [slots][8]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(fac + kFusedSlots * 8);
+    volatile int* aborted = reinterpret_cast<volatile int*>(bars + 2 * kFusedMaxStages + 3 * kFusedSlots);
+    uint8_t* ring = smem + (kFusedFixed + 127) / 128 * 128;
+    auto bar = [&](int s) { return smem_u32(bars + s); };
+    auto full = [&](int s) { return bar(s); };
+    auto empty = [&](int s) { return bar(kFusedMaxStages + s); };
+    auto parts = [&](int i) { return bar(2 * kFusedMaxStages + i % kFusedSlots); };
+    auto sums_in = [&](int i) { return bar(2 * kFusedMaxStages + kFusedSlots + i % kFusedSlots); };
+    auto factors = [&](int i) { return bar(2 * kFusedMaxStages + 2 * kFusedSlots + i % kFusedSlots); };
+    auto slot_phase = [&](int i) { return (uint32_t)(i / kFusedSlots) & 1u; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full(s), kSaved == kSavedMx ? 33u : 1u);
+            mbar_init(empty(s), (uint32_t)warps);
+        }
+        for (int s = 0; s < kFusedSlots; ++s) {
+            mbar_init(parts(s), (uint32_t)warps);
+            mbar_init(sums_in(s), (uint32_t)cs);
+            mbar_init(factors(s), 1u);
+        }
+        *aborted = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (cs > 1) cluster_sync();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int64_t cluster = blockIdx.x / cs, clusters = gridDim.x / cs;
+    const int n = (int)((a.T - cluster + clusters - 1) / clusters);
+    auto token = [&](int i) { return cluster + (int64_t)i * clusters; };
+    // Bounded waits of all 32 lanes; after one ran out every other ends too.
+    auto ready = [&](bool ok) {
+        if (ok) return true;
+        *aborted = 1;
+        atomicOr(a.err, kErrTimeout);
+        return false;
+    };
+    auto wait = [&](uint32_t b, uint32_t phase) {
+        return __all_sync(0xFFFFFFFFu, ready(mbar_wait(b, phase, aborted, a.wait_limit_ns)));
+    };
+
+    if (warp == loader) {
+        // rows of a stage: hidden [hc], keys and value [hc + 1], dout [hc]
+        const int rows = 3 * hc + 1;
+        for (int i = 0; i < n; ++i) {
+            const int s = i % stages;
+            if (!wait(empty(s), ((uint32_t)(i / stages) & 1u) ^ 1u)) break;
+            const int64_t t = token(i);
+            const uint32_t base = smem_u32(ring + s * stage_bytes);
+            if (lane == 0) mbar_expect_tx(full(s), (uint32_t)(fused_row_bytes<kSaved>(hc) * cols));
+            __syncwarp();
+            for (int r = lane; r < rows; r += 32) {
+                const char* src;
+                int size, off;  // bytes per value; of the row within the stage
+                if (r >= 2 * hc + 1) {
+                    const int b = r - (2 * hc + 1);
+                    size = 2;
+                    src = reinterpret_cast<const char*>(a.dout + (t * hc + b) * d);
+                    off = (fused_row_bytes<kSaved>(hc) - 2 * hc + 2 * b) * max_cols;
+                } else if (kSaved == kSavedMx) {
+                    size = 1;
+                    src = reinterpret_cast<const char*>(a.codes + (t * (2 * hc + 1) + r) * d);
+                    off = r * max_cols;
+                } else if (r < hc) {
+                    size = 2;
+                    src = reinterpret_cast<const char*>(a.hidden + (t * hc + r) * d);
+                    off = 2 * r * max_cols;
+                } else {
+                    size = kSaved == kSavedF32 ? 4 : 2;
+                    src = static_cast<const char*>(a.kv) + (t * (hc + 1) + (r - hc)) * d * size;
+                    off = (2 * hc + size * (r - hc)) * max_cols;
+                }
+                bulk_load(base + (uint32_t)off, src + (int64_t)col0 * size, (uint32_t)(cols * size), full(s));
+            }
+            if (kSaved == kSavedMx) {  // the exponents, 4 at a time
+                const uint32_t dst = base + (uint32_t)(fused_row_bytes<kSaved>(hc) * max_cols);
+                const int per = cols / 128, all = (2 * hc + 1) * per;
+                for (int x = lane; x < all; x += 32) {
+                    const int r = x / per, c = x - r * per;
+                    const uint8_t* src = a.scales + (t * (2 * hc + 1) + r) * (d / 32) + col0 / 32 + 4 * c;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                     dst + (uint32_t)(r * (max_cols / 32) + 4 * c)),
+                                 "l"(src)
+                                 : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full(s))
+                             : "memory");
+            }
+        }
+        if (kSaved == kSavedMx) asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == joiner) {
+        for (int i = 0; i < n; ++i) {
+            const int slot = i % kFusedSlots;
+            if (!wait(parts(i), slot_phase(i))) break;
+            float s = 0.f;
+            if (lane < kSums)
+                for (int x = 0; x < warps; ++x) s += wred[(slot * kFusedMaxWarps + x) * 32 + lane];
+            float* out = red + (slot * 8 + rank) * 32 + lane;
+            if (cs == 1) {
+                *out = s;
+                __syncwarp();
+            } else {
+                const uint32_t at = smem_u32(out);
+                for (int r = 0; r < cs; ++r)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)r)), "f"(s)
+                                 : "memory");
+                __syncwarp();
+                if (lane < cs) mbar_arrive_cluster(map_rank(sums_in(i), (uint32_t)lane));
+                if (!__all_sync(0xFFFFFFFFu, ready(mbar_wait_cluster(sums_in(i), slot_phase(i), aborted,
+                                                                     a.wait_limit_ns))))
+                    break;
+            }
+            if (lane < hc) {
+                float x[4] = {};
+                for (int r = 0; r < cs; ++r) {
+                    const float4 y = *reinterpret_cast<const float4*>(red + (slot * 8 + r) * 32 + 4 * lane);
+                    x[0] += y.x; x[1] += y.y; x[2] += y.z; x[3] += y.w;
+                }
+                fac[slot * 8 + lane] = gate_factors(x[0], x[1], x[2], x[3], d, a.eps);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(factors(i));
+        }
+    } else if (warp < warps) {
+        const int lc = warp * 256 + lane * 8;  // column within the CTA's range
+        f32x2 w[kHc][4], acc[kHc][4];
+#pragma unroll
+        for (int b = 0; b < kHc; ++b) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[b][j] = 0ull;
+            if (kExact || b < hc) {
+                float f[8];
+                load8_f32(a.wqk + (int64_t)b * d + col0 + lc, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[b][j] = pair(f[2 * j], f[2 * j + 1]);
+            }
+        }
+        // row r (hidden [hc], keys and value [hc + 1]) of a stage, this thread's
+        // columns, without the scale that is returned
+        auto saved = [&](const uint8_t* st, int r, f32x2 (&f)[4]) {
+            if (kSaved == kSavedMx) {
+                decode8(*reinterpret_cast<const uint2*>(st + r * max_cols + lc), f);
+                return e8m0_to_f32(st[fused_row_bytes<kSaved>(hc) * max_cols + r * (max_cols / 32) + lc / 32]);
+            }
+            if (r < hc || kSaved == kSavedBf16) {
+                unpack8(*reinterpret_cast<const uint4*>(st + 2 * (r * max_cols + lc)), f);
+            } else {
+                const ulonglong2* p = reinterpret_cast<const ulonglong2*>(st + 2 * hc * max_cols +
+                                                                          4 * ((r - hc) * max_cols + lc));
+                f[0] = p[0].x; f[1] = p[0].y; f[2] = p[1].x; f[3] = p[1].y;
+            }
+            return 1.0f;
+        };
+        auto dout = [&](const uint8_t* st, int b) {
+            return *reinterpret_cast<const uint4*>(
+                st + (fused_row_bytes<kSaved>(hc) - 2 * hc + 2 * b) * max_cols + 2 * lc);
+        };
+        for (int i = 0; i <= n; ++i) {
+            const bool image = i > 0 && a.windows[token(i - 1)].x == kDead;  // of phase 2's token
+            if (i < n) {
+                const int s = i % stages;
+                const uint8_t* st = ring + s * stage_bytes;
+                if (!wait(full(s), (uint32_t)(i / stages) & 1u)) break;
+                float sum[kSums];
+                f32x2 v[4];
+                const float cv = saved(st, 2 * hc, v);
+#pragma unroll
+                for (int b = 0; b < kHc; ++b) {
+                    float* sb = sum + 4 * b;
+                    sb[0] = sb[1] = sb[2] = sb[3] = 0.f;
+                    if (!kExact && b >= hc) continue;
+                    f32x2 h[4], k[4], dy[4];
+                    const float ch = saved(st, b, h), ck = saved(st, hc + b, k);
+                    unpack8(dout(st, b), dy);
+                    f32x2 q[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        q[0] = fma2(k[j], k[j], q[0]);
+                        q[1] = fma2(h[j], h[j], q[1]);
+                        q[2] = fma2(mul2(h[j], w[b][j]), k[j], q[2]);
+                        q[3] = fma2(dy[j], v[j], q[3]);
+                    }
+                    sb[0] = both(q[0]);
+                    sb[1] = both(q[1]);
+                    sb[2] = both(q[2]);
+                    sb[3] = both(q[3]);
+                    if (kSaved == kSavedMx) {
+                        sb[0] *= ck * ck;
+                        sb[1] *= ch * ch;
+                        sb[2] *= ch * ck;
+                        sb[3] *= cv;
+                    }
+                }
+                const float mine = warp_sums<kSums>(sum, lane);
+                constexpr int kPer = 32 / kSums;
+                if (lane % kPer == 0)
+                    wred[((i % kFusedSlots) * kFusedMaxWarps + warp) * 32 + lane / kPer] = mine;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(parts(i));
+            }
+            if (i == 0) continue;
+            const int p = i - 1, s = p % stages;
+            const uint8_t* st = ring + s * stage_bytes;
+            const int64_t t = token(p);
+            if (!wait(factors(p), slot_phase(p))) break;
+            const float4* fp = fac + (p % kFusedSlots) * 8;
+            uint16_t* dh_t = a.dhidden + t * (int64_t)hc * d + col0 + lc;
+            uint16_t* dkv_t = a.dkv + t * (int64_t)(hc + 1) * d + col0 + lc;
+            f32x2 dv[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int b = 0; b < kHc; ++b) {
+                if (!kExact && b >= hc) continue;
+                const uint4 raw = dout(st, b);
+                uint4 odh = raw, odk = make_uint4(0u, 0u, 0u, 0u);
+                if (!image) {
+                    const float4 f = fp[b];
+                    f32x2 dy[4], h[4], k[4], dh[4], dk[4];
+                    unpack8(raw, dy);
+                    const float ch = saved(st, b, h), ck = saved(st, hc + b, k);
+                    const float xk = f.x * ck, xh = f.x * ch, yh = -f.y * ch, zk = -f.z * ck, xhk = xk * ch;
+                    const f32x2 xk2 = pair(xk, xk), xh2 = pair(xh, xh), yh2 = pair(yh, yh), zk2 = pair(zk, zk),
+                                xhk2 = pair(xhk, xhk), g2 = pair(f.w, f.w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dh[j] = fma2(xk2, mul2(w[b][j], k[j]), fma2(yh2, h[j], dy[j]));
+                        dk[j] = fma2(xh2, mul2(w[b][j], h[j]), mul2(zk2, k[j]));
+                        dv[j] = fma2(g2, dy[j], dv[j]);
+                        acc[b][j] = fma2(xhk2, mul2(h[j], k[j]), acc[b][j]);
+                    }
+                    odh = pack8(dh);
+                    odk = pack8(dk);
+                }
+                __stcs(reinterpret_cast<uint4*>(dh_t + (int64_t)b * d), odh);
+                __stcs(reinterpret_cast<uint4*>(dkv_t + (int64_t)b * d), odk);
+            }
+            __stcs(reinterpret_cast<uint4*>(dkv_t + (int64_t)hc * d), pack8(dv));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(s));
+        }
+        float* part = a.dw_part + cluster * hc * d + col0 + lc;
+#pragma unroll
+        for (int b = 0; b < kHc; ++b)
+            if (kExact || b < hc) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = unpair(acc[b][j]);
+                    f[2 * j] = x.x;
+                    f[2 * j + 1] = x.y;
+                }
+                store8_f32(part + (int64_t)b * d, f);
+            }
+    }
+    __syncthreads();
+    if (*aborted) {  // let copies in flight land
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+        __syncthreads();
+    }
+    if (cs > 1) cluster_sync();  // no arrival may target a CTA that exited
+}
+
+// Cluster size and stages of the fused kernel for a geometry; 0 if none holds
+// three stages of a token (one in each phase and one on its way).
+template <int kSaved>
+int fused_cluster(int hc, int d, int* stages) {
+    const int groups = d / 256;
+    for (int cs = 1; cs <= 8 && cs <= groups; cs *= 2) {
+        const int per = (groups + cs - 1) / cs;
+        const int n = (227 * 1024 - kFusedFixed - 128) / fused_stage_bytes<kSaved>(hc, per * 256);
+        if (per <= kFusedMaxWarps && n >= 3) {
+            *stages = std::min(n, 6);
+            return cs;
+        }
+    }
+    return 0;
+}
+
+template <int kSaved, int kHc>
+cudaError_t fused_launch(GateTrain& a, int cs, int stages, int* shares, cudaStream_t s) {
+    auto kern = a.hc == kHc ? k_gate_backward_fused<kSaved, kHc, true> : k_gate_backward_fused<kSaved, kHc, false>;
+    const int per = (a.d / 256 + cs - 1) / cs;
+    const int smem = (kFusedFixed + 127) / 128 * 128 + stages * fused_stage_bytes<kSaved>(a.hc, per * 256);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    const int clusters = (int)std::min<int64_t>(a.T, device_sm_count() / cs);
+    cfg.gridDim = dim3(clusters * cs);
+    cfg.blockDim = dim3((per + 2) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    *shares = clusters;
+    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs);
+}
+
+// ---- two passes: geometries whose tokens do not fit ------------------------------------------
 // The factors of every token and branch: one block per token.
 template <int kSaved>
 __global__ void __launch_bounds__(320)
@@ -731,22 +1175,49 @@ k_gate_backward_columns(const GateTrain a) {
         if (b < hc) store8_f32(part + (int64_t)b * d, acc[b]);
 }
 
-// dwq = wk sum, dwk = wq sum, the shares added in order.
+// dwq = wk sum, dwk = wq sum over the shares: a block takes 128 columns, each of
+// its eight warps every eighth share in order, then the warps' sums in order.
 __global__ void __launch_bounds__(256)
 k_gate_backward_weights(const GateTrain a, int shares) {
     pdl_wait();
-    const int64_t n = (int64_t)a.hc * a.d;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < shares; ++p) s += __ldcg(a.dw_part + p * n + i);
-    if (a.dwq) a.dwq[i] = s * a.wk[i];
-    if (a.dwk) a.dwk[i] = s * a.wq[i];
+    __shared__ float4 sm[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = (int64_t)a.hc * a.d, i = (int64_t)blockIdx.x * 128 + lane * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = warp; p < shares; p += 8) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.dw_part + p * n + i));
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    sm[warp][lane] = s;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < 8; ++w) {
+        const float4 x = sm[w][lane];
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    auto put = [&](float* out, const float* w) {
+        if (!out) return;
+        const float4 x = *reinterpret_cast<const float4*>(w + i);
+        *reinterpret_cast<float4*>(out + i) = make_float4(s.x * x.x, s.y * x.y, s.z * x.z, s.w * x.w);
+    };
+    put(a.dwq, a.wk);
+    put(a.dwk, a.wq);
 }
 
 template <int kSaved>
-cudaError_t gate_backward(const GateTrain& a, int shares, cudaStream_t s) {
+cudaError_t gate_backward(GateTrain a, cudaStream_t s) {
+    const dim3 wgrid((unsigned)((int64_t)a.hc * a.d / 128));
+    int stages = 0, shares = 0;
+    if (const int cs = fused_cluster<kSaved>(a.hc, a.d, &stages)) {
+        cudaError_t e = a.hc == 1   ? fused_launch<kSaved, 1>(a, cs, stages, &shares, s)
+                        : a.hc == 2 ? fused_launch<kSaved, 2>(a, cs, stages, &shares, s)
+                        : a.hc <= 4 ? fused_launch<kSaved, 4>(a, cs, stages, &shares, s)
+                                    : fused_launch<kSaved, 8>(a, cs, stages, &shares, s);
+        if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;
+        return pdl_launch(k_gate_backward_weights, wgrid, dim3(256), 0, s, a, shares);
+    }
+    shares = gate_backward_shares(a.T, a.d);
     const int chunks = a.d / 8;
     cudaError_t e = pdl_launch(k_gate_backward_sums<kSaved>, dim3((unsigned)a.T),
                                dim3(std::min(320, chunks)), 0, s, a);
@@ -758,9 +1229,8 @@ cudaError_t gate_backward(const GateTrain& a, int shares, cudaStream_t s) {
              : a.hc <= 4 ? k_gate_backward_columns<kSaved, 4>
                          : k_gate_backward_columns<kSaved, 8>;
     e = pdl_launch(f, grid, dim3(threads), 0, s, a);
-    if (e != cudaSuccess) return e;
-    return pdl_launch(k_gate_backward_weights, dim3((unsigned)(((int64_t)a.hc * a.d + 255) / 256)),
-                      dim3(256), 0, s, a, shares);
+    if (e != cudaSuccess || (!a.dwq && !a.dwk)) return e;
+    return pdl_launch(k_gate_backward_weights, wgrid, dim3(256), 0, s, a, shares);
 }
 
 int log2_ceil(int64_t x) {
@@ -832,14 +1302,14 @@ cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t
 
 int gate_backward_shares(int64_t T, int d) {
     const int blocks = (d / 8 + 127) / 128;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(T, device_sm_count() * 4 / blocks));
+    // (the fused kernel's clusters are no more than the SMs)
+    return (int)std::max<int64_t>(1, std::min<int64_t>(T, device_sm_count() * std::max(1, 4 / blocks)));
 }
 
 cudaError_t launch_gate_backward(const GateTrain& a, int saved, cudaStream_t s) {
-    const int shares = gate_backward_shares(a.T, a.d);
-    if (saved == kSavedMx) return gate_backward<kSavedMx>(a, shares, s);
-    if (saved == kSavedF32) return gate_backward<kSavedF32>(a, shares, s);
-    return gate_backward<kSavedBf16>(a, shares, s);
+    if (saved == kSavedMx) return gate_backward<kSavedMx>(a, s);
+    if (saved == kSavedF32) return gate_backward<kSavedF32>(a, s);
+    return gate_backward<kSavedBf16>(a, s);
 }
 
 }  // namespace engram

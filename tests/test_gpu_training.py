@@ -358,6 +358,12 @@ def test_gate_backward(T, hc, d, saved):
     s.close()
 
 
+@pytest.mark.parametrize("saved", ["f32", "bf16", "mxfp8"])
+@pytest.mark.parametrize("T,hc,d", [(700, 2, 256), (320, 4, 5120), (3, 8, 9216), (2, 1, 20_736)])
+def test_gate_backward_of_many_and_of_wide_tokens(T, hc, d, saved):
+    test_gate_backward(T, hc, d, saved)
+
+
 def test_gate_backward_against_differences():
     """The kernel's gradient against central differences of the step in 64 bits."""
     T, hc, d = 2, 2, 256
