@@ -45,6 +45,7 @@ engram_status check_embed(uint64_t rows, uint32_t dim, int64_t n, uint32_t copie
     if (dim < 8 || dim % 8 || dim > 65536) return fail(ENGRAM_EINVAL, "dim must be a multiple of 8 in [8, 65536]");
     if (n < 0 || n > (int64_t)1 << 30) return fail(ENGRAM_EINVAL, "n must be in [0, 2^30]");
     if (copies < 1 || copies > 8) return fail(ENGRAM_EINVAL, "copies must be in [1, 8]");
+    if ((uint64_t)n * copies >= 1ull << 32) return fail(ENGRAM_EINVAL, "n x copies must be below 2^32");
     return ENGRAM_OK;
 }
 
@@ -74,7 +75,9 @@ EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
     w.segpos = c.take<uint32_t>(n);
     w.seg_start = c.take<uint32_t>(n + 1);
     w.unique = c.take<uint32_t>(n);
-    const int64_t chunks = ceil_div(n, embed_rows_per_chunk(n, (int)dim, 1));
+    int64_t chunks = 0;  // of any number of copies
+    for (int copies = 1; copies <= 8; ++copies)
+        chunks = std::max(chunks, ceil_div(n, embed_rows_per_chunk(n, (int)dim, copies)));
     w.partial = c.take<float>((size_t)chunks * 2 * dim);
     w.bytes = c.at;
     return w;

@@ -84,6 +84,8 @@ k_embed(const void* __restrict__ table, uint64_t rows, int dim, const uint32_t* 
 
 // ---- sort of the ids -------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kSortBatch = 8;  // rounds of 32 keys that a warp loads at once
+constexpr int kSmallSort = kSortThreads * 8;  // keys of the one-cluster sort
 
 // A barrier of the cooperative launch's blocks, bounded: false on a time-out.
 __device__ __forceinline__ bool grid_barrier(const EmbedSort& a, uint32_t& phase, int* flag) {
@@ -110,21 +112,121 @@ __device__ __forceinline__ bool grid_barrier(const EmbedSort& a, uint32_t& phase
     return *flag == 0;
 }
 
+// The lanes whose digit equals this lane's (of `bits` bits), among the `on`
+// lanes: one vote per bit (faster than match.any: 27 us against 33 for the sort
+// of 8,192 ids in one block).
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, int bits, uint32_t on) {
+    uint32_t same = on;
+#pragma unroll
+    for (int b = 0; b < 9; ++b) {
+        if (b < bits) {
+            const bool set = (d >> b) & 1u;
+            const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
+            same &= set ? v : ~v;
+        }
+    }
+    return same;
+}
+
+// Exclusive sums over the block of one value per thread; *all gets the total.
+__device__ __forceinline__ uint32_t block_scan(uint32_t c, uint32_t* warp_sum, uint32_t* all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    __syncthreads();  // what an earlier call left in warp_sum is read
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    const uint32_t s = warp_sum[lane];
+    const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s : 0u);
+    *all = __reduce_add_sync(0xFFFFFFFFu, s);
+    return before + inc - c;
+}
+
+// Exclusive sums of each digit's counts over the warps, in place; the digit's
+// total for the thread that holds it (bins <= 512 of the 1,024 threads).
+__device__ __forceinline__ uint32_t scan_warps(uint32_t* cnt, int bins) {
+    uint32_t total = 0;
+    if ((int)threadIdx.x < bins) {
+#pragma unroll
+        for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+            uint32_t c[16];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) c[w] = cnt[(w0 + w) * bins + threadIdx.x];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                cnt[(w0 + w) * bins + threadIdx.x] = total;
+                total += c[w];
+            }
+        }
+    }
+    return total;
+}
+__device__ __forceinline__ void add_warps(uint32_t* cnt, int bins, uint32_t base) {
+    if ((int)threadIdx.x < bins) {
+#pragma unroll 16
+        for (int w = 0; w < kSortWarps; ++w) cnt[w * bins + threadIdx.x] += base;
+    }
+}
+
+// Eight neighbouring sorted keys (from place i0) and the ones beside them: which
+// of them begin a segment, and where the ids of table rows end.
+struct Heads {
+    uint32_t key[kSortBatch];
+    uint32_t begins;  // bit u: place i0 + u begins a segment
+    uint32_t last;    // bit u: place i0 + u holds the last id of a table row
+};
+__device__ __forceinline__ Heads find_heads(const uint32_t (&key)[kSortBatch], uint32_t before,
+                                            uint32_t after, int64_t i0, int64_t end, uint32_t rows) {
+    Heads h;
+    h.begins = h.last = 0;
+    uint32_t prev = before;
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u) {
+        h.key[u] = key[u];
+        const bool valid = i0 + u < end && key[u] < rows;
+        const uint32_t next = u + 1 < kSortBatch ? key[u + 1 < kSortBatch ? u + 1 : u] : after;
+        if (valid && (i0 + u == 0 || key[u] != prev)) h.begins |= 1u << u;
+        if (valid && (i0 + u + 1 >= end || next >= rows)) h.last |= 1u << u;
+        prev = key[u];
+    }
+    return h;
+}
+// Writes the segments of those places; `seg` is the number of segments before them.
+__device__ __forceinline__ void put_segments(const EmbedSort& a, const Heads& h, int64_t i0, int64_t end,
+                                             uint32_t seg) {
+#pragma unroll
+    for (int u = 0; u < kSortBatch; ++u) {
+        const int64_t i = i0 + u;
+        if (i >= end || h.key[u] >= (uint32_t)a.rows) continue;
+        if ((h.begins >> u) & 1u) {
+            a.unique[seg] = h.key[u];
+            a.seg_start[seg] = (uint32_t)i;
+            ++seg;
+        }
+        a.segpos[i] = seg - 1u;
+    }
+}
+
 // Stable radix sort of (id, position), least significant digit first, then the
 // segments of equal ids.  A block owns a contiguous range of the keys and a
 // warp a contiguous part of it, so the order of equal digits is kept: per pass,
-// every warp counts its digits (lanes with equal digits found by match_any, one
-// of them adds their number), the counts are turned into first places over
-// (digit, block, warp), and each warp hands them out in key order.  Ids that
-// are masked or outside the table become `rows`, the largest key: they sort
-// behind every row and take no part.
+// every warp counts its digits (one of the lanes with equal digits adds their
+// number), the counts are turned into first places over (digit, block, warp),
+// and each warp hands them out in key order.  Ids that are masked or outside
+// the table become `rows`, the largest key: they sort behind every row and take
+// no part.  kOne: a warp's keys are one batch, which stays in registers with the
+// places found while counting.
+template <bool kOne>
 __global__ void __launch_bounds__(kSortThreads)
 k_embed_sort(const EmbedSort a) {
     extern __shared__ uint32_t cnt[];  // [kSortWarps][bins]
     __shared__ uint32_t warp_sum[kSortWarps];
     __shared__ uint32_t shared_base;
     __shared__ int flag;
-    pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t lt = (1u << lane) - 1u;
     const int B = (int)gridDim.x, b = (int)blockIdx.x;
@@ -139,6 +241,7 @@ k_embed_sort(const EmbedSort a) {
     if (threadIdx.x == 0) flag = 0;
     __syncthreads();
     const uint32_t rows = (uint32_t)a.rows;
+    uint32_t* const mine = cnt + warp * bins;
 
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * a.digit_bits;
@@ -146,36 +249,48 @@ k_embed_sort(const EmbedSort a) {
         const uint32_t* vin = pass & 1 ? a.vals1 : a.vals0;
         uint32_t* kout = pass & 1 ? a.keys0 : a.keys1;
         uint32_t* vout = pass & 1 ? a.vals0 : a.vals1;
-        auto key = [&](int64_t i) {
-            if (pass) return __ldcg(kin + i);
-            const uint32_t id = a.ids[i];
-            return id < rows ? id : rows;
+        uint32_t k[kSortBatch], v[kSortBatch], at[kSortBatch];
+        auto load = [&](int64_t r) {
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                const int64_t i = (r + u) * 32 + lane;
+                k[u] = v[u] = 0u;
+                if (r + u < w1 && i < a.n) {
+                    k[u] = pass ? __ldcg(kin + i) : min(a.ids[i], rows);
+                    v[u] = pass ? __ldcg(vin + i) : (uint32_t)i;
+                }
+            }
+        };
+        auto rank = [&](int64_t r) {
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                const bool on = r + u < w1 && (r + u) * 32 + lane < a.n;
+                const uint32_t all_on = __ballot_sync(0xFFFFFFFFu, on);
+                const uint32_t d = (k[u] >> shift) & dmask;
+                const uint32_t same = same_digit(d, a.digit_bits, all_on);
+                at[u] = on ? mine[d] + __popc(same & lt) : 0u;
+                __syncwarp();
+                if (on && (same & lt) == 0u) mine[d] += __popc(same);
+                __syncwarp();
+            }
         };
         for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
         __syncthreads();
-        uint32_t* mine = cnt + warp * bins;
-        for (int64_t r = w0; r < w1; ++r) {
-            const int64_t i = r * 32 + lane;
-            const bool on = i < a.n;
-            if (pass == 0 && on) {
-                const uint32_t id = a.ids[i];
-                if (id >= rows && id != kMasked) atomicOr(a.err, kErrBounds);
+        for (int64_t r = w0; r < w1; r += kSortBatch) {
+            load(r);
+            if (pass == 0) {
+#pragma unroll
+                for (int u = 0; u < kSortBatch; ++u) {
+                    const int64_t i = (r + u) * 32 + lane;
+                    if (r + u < w1 && i < a.n && k[u] == rows && a.ids[i] != kMasked)
+                        atomicOr(a.err, kErrBounds);
+                }
             }
-            const uint32_t d = on ? (key(i) >> shift) & dmask : 0xFFFFFFFFu;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
-            if (on && (same & lt) == 0u) mine[d] += __popc(same);
-            __syncwarp();
+            rank(r);
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < bins; d += kSortThreads) {
-            uint32_t s = 0;
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = cnt[w * bins + d];
-                cnt[w * bins + d] = s;
-                s += c;
-            }
-            __stcg(a.hist + (int64_t)d * B + b, s);
-        }
+        const uint32_t total = scan_warps(cnt, bins);
+        if ((int)threadIdx.x < bins) __stcg(a.hist + (int64_t)threadIdx.x * B + b, total);
         if (!grid_barrier(a, phase, &flag)) return;
         // first place of each (digit, block) within its digit
         for (int d = b * kSortWarps + warp; d < bins; d += B * kSortWarps) {
@@ -195,75 +310,50 @@ k_embed_sort(const EmbedSort a) {
             if (lane == 0) __stcg(a.digit_total + d, run);
         }
         if (!grid_barrier(a, phase, &flag)) return;
-        // places over the digits (bins <= 1,024: one digit per thread)
-        {
-            const int d = threadIdx.x;
-            const uint32_t c = d < bins ? __ldcg(a.digit_total + d) : 0u;
-            uint32_t inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if (lane >= o) inc += y;
+        const int d = (int)threadIdx.x;
+        uint32_t all;
+        const uint32_t base = block_scan(d < bins ? __ldcg(a.digit_total + d) : 0u, warp_sum, &all);
+        add_warps(cnt, bins, d < bins ? base + __ldcg(a.hist + (int64_t)d * B + b) : 0u);
+        __syncthreads();
+        for (int64_t r = w0; r < w1; r += kSortBatch) {
+            if (!kOne) {
+                load(r);
+                rank(r);
             }
-            if (lane == 31) warp_sum[warp] = inc;
-            __syncthreads();
-            if (warp == 0) {
-                const uint32_t s = warp_sum[lane];
-                uint32_t si = s;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, si, o);
-                    if (lane >= o) si += y;
+            for (int u = 0; u < kSortBatch; ++u) {
+                if (r + u < w1 && (r + u) * 32 + lane < a.n) {
+                    const uint32_t p = at[u] + (kOne ? mine[(k[u] >> shift) & dmask] : 0u);
+                    __stcg(kout + p, k[u]);
+                    __stcg(vout + p, v[u]);
                 }
-                warp_sum[lane] = si - s;
-            }
-            __syncthreads();
-            if (d < bins) {
-                const uint32_t base = warp_sum[warp] + inc - c + __ldcg(a.hist + (int64_t)d * B + b);
-                for (int w = 0; w < kSortWarps; ++w) cnt[w * bins + d] += base;
-            }
-            __syncthreads();
-        }
-        for (int64_t r = w0; r < w1; ++r) {
-            const int64_t i = r * 32 + lane;
-            const bool on = i < a.n;
-            const uint32_t k = on ? key(i) : 0u;
-            const uint32_t v = on ? (pass ? __ldcg(vin + i) : (uint32_t)i) : 0u;
-            const uint32_t d = on ? (k >> shift) & dmask : 0xFFFFFFFFu;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
-            uint32_t at = 0;
-            if (on) at = mine[d] + __popc(same & lt);
-            __syncwarp();
-            if (on && (same & lt) == 0u) mine[d] += __popc(same);
-            __syncwarp();
-            if (on) {
-                __stcg(kout + at, k);
-                __stcg(vout + at, v);
             }
         }
         if (!grid_barrier(a, phase, &flag)) return;
     }
 
-    // segments of equal ids among the n_valid ids of table rows
+    // segments of equal ids among the ids of table rows
     const uint32_t* keys = a.passes & 1 ? a.keys1 : a.keys0;
-    auto head = [&](int64_t i, uint32_t k) {
-        return k < rows && (i == 0 || __ldcg(keys + i - 1) != k);
+    const int64_t lo = r0 * 32, hi = min(r1 * 32, a.n);
+    auto heads_at = [&](int64_t i0) {
+        uint32_t key[kSortBatch];
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) key[u] = i0 + u < hi ? __ldcg(keys + i0 + u) : rows;
+        const uint32_t before = i0 > 0 && i0 < hi ? __ldcg(keys + i0 - 1) : rows;
+        const uint32_t after = i0 + kSortBatch < a.n ? __ldcg(keys + i0 + kSortBatch) : rows;
+        // (hi is a multiple of eight unless it is n: `after` is the next place's key)
+        return find_heads(key, before, after, i0, hi < a.n && i0 + kSortBatch >= hi ? hi + 1 : hi, rows);
     };
-    const int64_t i0 = r0 * 32, i1 = min(r1 * 32, a.n);
     uint32_t heads = 0;
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
-        const uint32_t k = __ldcg(keys + i);
-        heads += head(i, k) ? 1u : 0u;
-        if (i == 0 && k >= rows) __stcg(a.n_valid, 0u);
-        if (k < rows && (i == a.n - 1 || __ldcg(keys + i + 1) >= rows)) __stcg(a.n_valid, (uint32_t)(i + 1));
+    for (int64_t i0 = lo + threadIdx.x * kSortBatch; i0 < hi; i0 += kSortThreads * kSortBatch) {
+        const Heads h = heads_at(i0);
+        heads += __popc(h.begins);
+        if (h.last) __stcg(a.n_valid, (uint32_t)(i0 + __ffs(h.last)));
     }
-    heads = __reduce_add_sync(0xFFFFFFFFu, heads);
-    if (lane == 0) warp_sum[warp] = heads;
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t s = __reduce_add_sync(0xFFFFFFFFu, warp_sum[lane]);
-        if (lane == 0) __stcg(a.block_heads + b, s);
-    }
+    if (b == 0 && threadIdx.x == 0 && __ldcg(keys) >= rows) __stcg(a.n_valid, 0u);
+    uint32_t block_heads;
+    block_scan(heads, warp_sum, &block_heads);
+    if (threadIdx.x == 0) __stcg(a.block_heads + b, block_heads);
     if (!grid_barrier(a, phase, &flag)) return;
     if (warp == 0) {
         uint32_t before = 0, all = 0;
@@ -284,27 +374,119 @@ k_embed_sort(const EmbedSort a) {
     }
     __syncthreads();
     uint32_t base = shared_base;
-    for (int64_t t0 = i0; t0 < i1; t0 += kSortThreads) {
-        const int64_t i = t0 + threadIdx.x;
-        const uint32_t k = i < i1 ? __ldcg(keys + i) : rows;
-        const bool h = i < i1 && head(i, k);
-        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, h);
-        __syncthreads();  // warp_sum of the round before is read
-        if (lane == 0) warp_sum[warp] = __popc(bal);
-        __syncthreads();
-        const uint32_t s = warp_sum[lane];
-        const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s : 0u);
-        const uint32_t round_all = __reduce_add_sync(0xFFFFFFFFu, s);
-        const uint32_t upto = base + before + __popc(bal & (lt | (1u << lane)));
-        if (i < i1 && k < rows) {
-            a.segpos[i] = upto - 1u;
-            if (h) {
-                a.unique[upto - 1u] = k;
-                a.seg_start[upto - 1u] = (uint32_t)i;
-            }
-        }
-        base += round_all;
+    for (int64_t t0 = lo; t0 < hi; t0 += kSortThreads * kSortBatch) {
+        const int64_t i0 = t0 + threadIdx.x * kSortBatch;
+        Heads h;
+        h.begins = 0;
+        if (i0 < hi) h = heads_at(i0);
+        uint32_t all;
+        const uint32_t before = block_scan(__popc(h.begins), warp_sum, &all);
+        if (i0 < hi) put_segments(a, h, i0, hi, base + before);
+        base += all;
     }
+}
+
+// The same sort for at most kSmallSort ids by one cluster, a key per thread: the
+// keys move between the CTAs' shared memories, no pass touches global memory.
+// (One block with eight keys a thread took 27 us for 8,192 ids, bound by its
+// issue rate.)
+__global__ void __launch_bounds__(kSortThreads)
+k_embed_sort_small(const EmbedSort a) {
+    extern __shared__ uint32_t cnt[];  // [kSortWarps][bins]
+    __shared__ uint32_t keys[2][kSortThreads], vals[2][kSortThreads];
+    __shared__ uint32_t totals[512];
+    __shared__ uint32_t warp_sum[kSortWarps];
+    __shared__ uint32_t edge[3];  // first and last key, segments that begin here
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lt = (1u << lane) - 1u;
+    const uint32_t rank = cluster_ctarank(), cs = gridDim.x;
+    const int n = (int)a.n, bins = 1 << a.digit_bits;
+    const uint32_t dmask = (uint32_t)bins - 1u, rows = (uint32_t)a.rows;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int i = (int)rank * kSortThreads + (int)threadIdx.x;
+    // keys beyond n are larger than any: they stay behind
+    uint32_t k = 0xFFFFFFFFu, v = (uint32_t)i;
+    if (i < n) {
+        const uint32_t id = a.ids[i];
+        k = min(id, rows);
+        if (id >= rows && id != kMasked) atomicOr(a.err, kErrBounds);
+    }
+    uint32_t* const mine = cnt + warp * bins;
+    auto remote = [&](const uint32_t* p, uint32_t r) {
+        uint32_t x;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(map_rank(smem_u32(p), r)) : "memory");
+        return x;
+    };
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const uint32_t d = (k >> (pass * a.digit_bits)) & dmask;
+        for (int x = lane; x < bins; x += 32) mine[x] = 0;
+        __syncwarp();
+        const uint32_t same = same_digit(d, a.digit_bits, 0xFFFFFFFFu);
+        if ((same & lt) == 0u) mine[d] = __popc(same);
+        __syncthreads();
+        const uint32_t total = scan_warps(cnt, bins);
+        if ((int)threadIdx.x < bins) totals[threadIdx.x] = total;
+        cluster_sync();
+        uint32_t before = 0, sum = 0;
+        if ((int)threadIdx.x < bins)
+            for (uint32_t r = 0; r < cs; ++r) {
+                const uint32_t c = remote(totals + threadIdx.x, r);
+                sum += c;
+                if (r < rank) before += c;
+            }
+        uint32_t all;
+        const uint32_t base = block_scan(sum, warp_sum, &all);
+        add_warps(cnt, bins, base + before);
+        __syncthreads();
+        const uint32_t p = mine[d] + __popc(same & lt);
+        const int to = pass & 1;
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(keys[to] + (p & 1023u)), p >> 10)),
+                     "r"(k)
+                     : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(vals[to] + (p & 1023u)), p >> 10)),
+                     "r"(v)
+                     : "memory");
+        cluster_sync();
+        k = keys[to][threadIdx.x];
+        v = vals[to][threadIdx.x];
+    }
+    // the sorted positions and the segments
+    if (i < n) (a.passes & 1 ? a.vals1 : a.vals0)[i] = v;
+    const int in = (a.passes - 1) & 1;
+    if (threadIdx.x == 0) edge[0] = k;
+    if (threadIdx.x == kSortThreads - 1) edge[1] = k;
+    cluster_sync();
+    const uint32_t prev = threadIdx.x ? keys[in][threadIdx.x - 1] : rank ? remote(edge + 1, rank - 1) : rows;
+    const uint32_t next = threadIdx.x + 1 < kSortThreads ? keys[in][threadIdx.x + 1]
+                          : rank + 1 < cs ? remote(edge, rank + 1) : rows;
+    const bool valid = i < n && k < rows, begins = valid && (i == 0 || k != prev);
+    uint32_t here;
+    uint32_t seg = block_scan(begins ? 1u : 0u, warp_sum, &here) + (begins ? 1u : 0u);
+    if (threadIdx.x == 0) edge[2] = here;
+    cluster_sync();
+    uint32_t all = 0;
+    for (uint32_t r = 0; r < cs; ++r) {
+        const uint32_t c = remote(edge + 2, r);
+        all += c;
+        if (r < rank) seg += c;
+    }
+    if (valid) {
+        a.segpos[i] = seg - 1u;
+        if (begins) {
+            a.unique[seg - 1u] = k;
+            a.seg_start[seg - 1u] = (uint32_t)i;
+        }
+        if (i + 1 == n || next >= rows) {
+            *a.n_valid = (uint32_t)(i + 1);
+            a.seg_start[all] = (uint32_t)(i + 1);
+        }
+    }
+    if (i == 0) {
+        *a.count = all;
+        if (all == 0) *a.n_valid = a.seg_start[0] = 0u;
+    }
+    cluster_sync();  // no CTA exits while another reads its shared memory
 }
 
 // ---- sums over the segments ---------------------------------------------------------------
@@ -315,7 +497,7 @@ k_embed_sort(const EmbedSort a) {
 // or tail (it begins here) - for k_embed_join, which adds them in order.  So no
 // sum depends on the order in which blocks run, and a hot id's rows are spread
 // over as many threads as a cold one's.
-constexpr int kSumBatch = 8;
+constexpr int kSumBatch = 8;  // rows loaded before they are added
 
 __device__ __forceinline__ void put_row(const EmbedSum& a, uint32_t seg, int col,
                                         const float (&acc)[8]) {
@@ -333,101 +515,156 @@ __device__ __forceinline__ void put_row(const EmbedSum& a, uint32_t seg, int col
     store8_f32(p, o);
 }
 
+// kC: copies, rounded up to 1, 2, 4 or 8.  Whether a segment crosses the chunk's
+// ends is known from the places beside it, so finishing a segment loads nothing.
+template <int kC>
 __global__ void __launch_bounds__(256)
 k_embed_sum(const EmbedSum a) {
     pdl_wait();
     pdl_launch_dependents();
+    constexpr int kPlaces = kSumBatch / kC;  // of a batch
     const int l = threadIdx.x % a.lanes;
     const int64_t work = ((int64_t)blockIdx.x * 256 + threadIdx.x) / a.lanes;
     const int64_t chunk = work / a.slices;
     const int col = ((int)(work - chunk * a.slices) * a.lanes + l) * 8;
     const int64_t nv = *a.n_valid;
-    const int64_t lo = chunk * a.rows_per_chunk, hi = min(lo + a.rows_per_chunk, nv);
-    if (lo >= hi || col >= a.dim) return;
+    const int64_t lo = chunk * a.rows_per_chunk;
+    // (a group beyond the last place, or a lane beyond dim, takes part in the
+    // shuffles with nothing to add)
+    const int count = (int)max((int64_t)0, min((int64_t)a.rows_per_chunk, nv - lo));
+    const bool in = count > 0 && col < a.dim;
     float acc[8] = {};
-    uint32_t cur = a.segpos[lo];
-    auto flush = [&](uint32_t seg) {
-        const int64_t s0 = a.seg_start[seg], s1 = a.seg_start[seg + 1];
-        if (s0 >= lo && s1 <= hi)
-            put_row(a, seg, col, acc);
-        else
-            store8_f32(a.partial + (2 * chunk + (s0 >= lo ? 1 : 0)) * a.dim + col, acc);
+    uint32_t cur = count > 0 ? a.segpos[lo] : 0u;
+    const uint32_t tail = count > 0 ? a.segpos[lo + count - 1] : 0u;
+    bool began_before = count > 0 && lo > 0 && a.segpos[lo - 1] == cur;
+    const bool goes_on = count > 0 && lo + count < nv && a.segpos[lo + count] == tail;
+    auto flush = [&](bool ends) {
+        if (in) {
+            if (ends && !began_before)
+                put_row(a, cur, col, acc);
+            else
+                store8_f32(a.partial + (2 * chunk + (began_before ? 0 : 1)) * a.dim + col, acc);
+        }
+        began_before = false;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     };
-    // rows are (place, copy) pairs, a batch of them loaded before they are added
-    const int64_t total = (hi - lo) * a.copies;
-    int64_t pos = lo;
-    int copy = 0;
-    for (int64_t q0 = 0; q0 < total; q0 += kSumBatch) {
-        uint4 v[kSumBatch];
-        uint32_t seg[kSumBatch];
+    // the group loads `lanes` places at a time, one per lane, the next ones while
+    // these are added
+    auto place = [&](int i, uint32_t& seg, uint32_t& row) {
+        seg = row = 0u;
+        if (i + l < count) {
+            seg = a.segpos[lo + i + l];
+            row = a.perm[lo + i + l];
+        }
+    };
+    uint32_t seg, row;
+    place(0, seg, row);
+    for (int i0 = 0; i0 < a.rows_per_chunk; i0 += a.lanes) {
+        uint32_t next_seg, next_row;
+        place(i0 + a.lanes, next_seg, next_row);
+        for (int j0 = 0; j0 < a.lanes; j0 += kPlaces) {
+            uint4 v[kPlaces][kC];
 #pragma unroll
-        for (int u = 0; u < kSumBatch; ++u) {
-            if (q0 + u < total) {
-                seg[u] = a.segpos[pos];
-                v[u] = __ldcs(reinterpret_cast<const uint4*>(
-                    a.dout + ((int64_t)a.perm[pos] * a.copies + copy) * a.dim + col));
-                if (++copy == a.copies) {
-                    copy = 0;
-                    ++pos;
+            for (int u = 0; u < kPlaces; ++u) {
+                const uint32_t r = __shfl_sync(0xFFFFFFFFu, row, j0 + u, a.lanes);
+                if (in && i0 + j0 + u < count && j0 + u < a.lanes) {
+                    const uint16_t* p = a.dout + (int64_t)r * a.copies * a.dim + col;
+#pragma unroll
+                    for (int c = 0; c < kC; ++c)
+                        if (c < a.copies) v[u][c] = __ldcs(reinterpret_cast<const uint4*>(p + (int64_t)c * a.dim));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kPlaces; ++u) {
+                const uint32_t sg = __shfl_sync(0xFFFFFFFFu, seg, j0 + u, a.lanes);
+                if (i0 + j0 + u < count && j0 + u < a.lanes) {
+                    if (sg != cur) {
+                        flush(true);
+                        cur = sg;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kC; ++c)
+                        if (c < a.copies) {
+                            float f[8];
+                            unpack8(v[u][c], f);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) acc[j] += f[j];
+                        }
                 }
             }
         }
-#pragma unroll
-        for (int u = 0; u < kSumBatch; ++u) {
-            if (q0 + u < total) {
-                if (seg[u] != cur) {
-                    flush(cur);
-                    cur = seg[u];
-                }
-                float f[8];
-                unpack8(v[u], f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] += f[j];
-            }
-        }
+        seg = next_seg;
+        row = next_row;
     }
-    flush(cur);
+    if (count > 0) flush(!goes_on);
 }
 
-// One block per (chunk, 256 columns): if a segment begins in the chunk and
-// leaves it, its row is the chunk's tail and the following chunks' heads, each
-// of the block's eight warps adding a contiguous share in order, the shares
-// then in order.
+// The rows of segments that cross chunks: a segment that begins in a chunk and
+// leaves it is that chunk's tail and the following chunks' heads, added in order.
+// A block looks at eight chunks, a warp at one: the warp adds a row of up to
+// kJoinAlone parts itself; a longer one (a hot id) is added by the block, each
+// warp a contiguous share, then the shares in order.
+constexpr int kJoinAlone = 32;
+
+__device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int64_t p0, int64_t p1, int col,
+                                          float (&acc)[8]) {
+    if (col >= a.dim) return;
+#pragma unroll 8
+    for (int64_t p = p0; p < p1; ++p) {
+        float x[8];
+        load8_f32(a.partial + (2 * (chunk + p) + (p == 0 ? 1 : 0)) * a.dim + col, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += x[j];
+    }
+}
+
 __global__ void __launch_bounds__(256)
-k_embed_join(const EmbedSum a) {
+k_embed_join(const EmbedSum a, int64_t chunks) {
     pdl_wait();
     __shared__ float sm[8][32][9];
-    const int64_t chunk = blockIdx.x;
+    __shared__ int64_t parts_of[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = ((int)blockIdx.y * 32 + lane) * 8;
     const int64_t nv = *a.n_valid;
+    const int64_t chunk = (int64_t)blockIdx.x * 8 + warp;
     const int64_t lo = chunk * a.rows_per_chunk, hi = lo + a.rows_per_chunk;
-    if (hi >= nv) return;  // (a last chunk's segment ends in it)
-    const uint32_t seg = a.segpos[hi - 1];
-    const int64_t s0 = a.seg_start[seg], s1 = a.seg_start[seg + 1];
-    if (s0 < lo || s1 <= hi) return;
-    const int64_t parts = (s1 - 1) / a.rows_per_chunk - chunk + 1;  // tail, then heads
-    const int64_t p0 = parts * warp / 8, p1 = parts * (warp + 1) / 8;
-    float acc[8] = {};
-    if (col < a.dim) {
-#pragma unroll 4
-        for (int64_t p = p0; p < p1; ++p) {
-            float x[8];
-            load8_f32(a.partial + (2 * (chunk + p) + (p == 0 ? 1 : 0)) * a.dim + col, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += x[j];
-        }
+    int64_t parts = 0;
+    uint32_t seg = 0;
+    if (chunk < chunks - 1) {
+        // (three independent loads; places past nv hold nothing)
+        seg = a.segpos[hi - 1];
+        const uint32_t next = a.segpos[hi];
+        const uint32_t prev = lo ? a.segpos[lo - 1] : 0xFFFFFFFFu;
+        if (hi < nv && next == seg && prev != seg)
+            parts = ((int64_t)a.seg_start[seg + 1] - 1) / a.rows_per_chunk - chunk + 1;  // tail, heads
     }
+    if (parts && parts <= kJoinAlone && col < a.dim) {
+        float acc[8] = {};
+        add_parts(a, chunk, 0, parts, col, acc);
+        put_row(a, seg, col, acc);
+    }
+    if (lane == 0) parts_of[warp] = parts > kJoinAlone ? parts : 0;
+    if (!__syncthreads_or(parts > kJoinAlone)) return;
+    for (int w = 0; w < 8; ++w) {
+        const int64_t all = parts_of[w];
+        if (!all) continue;
+        float acc[8] = {};
+        add_parts(a, (int64_t)blockIdx.x * 8 + w, all * warp / 8, all * (warp + 1) / 8, col, acc);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sm[warp][lane][j] = acc[j];
-    __syncthreads();
-    if (warp || col >= a.dim) return;
-    for (int w = 1; w < 8; ++w)
+        for (int j = 0; j < 8; ++j) sm[warp][lane][j] = acc[j];
+        __syncthreads();
+        if (warp == w && col < a.dim) {
+            float sum[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += sm[w][lane][j];
-    put_row(a, seg, col, acc);
+            for (int j = 0; j < 8; ++j) sum[j] = sm[0][lane][j];
+            for (int x = 1; x < 8; ++x)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += sm[x][lane][j];
+            put_row(a, seg, col, sum);
+        }
+        __syncthreads();
+    }
 }
 
 // ---- 8-bit blocks ---------------------------------------------------------------------------
@@ -1262,26 +1499,51 @@ void embed_sort_digits(uint64_t rows, int* passes, int* bits) {
 }
 
 cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
+    if (a.n <= kSmallSort) {
+        const int smem = kSortWarps * (1 << a.digit_bits) * 4;
+        cudaError_t e = cudaFuncSetAttribute(k_embed_sort_small,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        unsigned cs = 1;
+        while (cs * kSortThreads < a.n) cs *= 2;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cs;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(cs);
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, k_embed_sort_small, a);
+    }
     const int blocks = embed_sort_blocks(a.n);
     const int smem = kSortWarps * (1 << a.digit_bits) * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // a warp's rounds of 32 keys, at most
+    const int64_t per_warp = (((a.n + 31) / 32 + blocks - 1) / blocks + kSortWarps - 1) / kSortWarps;
+    auto f = per_warp <= kSortBatch ? k_embed_sort<true> : k_embed_sort<false>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a.barrier, 0, 4, s);
     if (e != cudaSuccess) return e;
-    if (blocks > 1) {
-        e = cudaMemsetAsync(a.barrier, 0, 4, s);
-        if (e != cudaSuccess) return e;
-        EmbedSort copy = a;
-        void* args[] = {&copy};
-        return cudaLaunchCooperativeKernel((void*)k_embed_sort, dim3(blocks), dim3(kSortThreads),
-                                           args, smem, s);
-    }
-    return pdl_launch(k_embed_sort, dim3(1), dim3(kSortThreads), smem, s, a);
+    EmbedSort copy = a;
+    void* args[] = {&copy};
+    return cudaLaunchCooperativeKernel((void*)f, dim3(blocks), dim3(kSortThreads), args, smem, s);
 }
 
+// Sorted places per chunk: 64 rows of dout (a chunk's two partial rows are then
+// a few percent of what it reads), fewer while the chunks do not fill the GPU
+// four times over.
 int embed_rows_per_chunk(int64_t n, int dim, int copies) {
-    (void)copies;
-    // long enough that partial sums are few beside the rows read, short enough
-    // that the chunks fill the GPU
-    return n * (int64_t)dim >= (int64_t)1 << 26 ? 64 : n * (int64_t)dim >= (int64_t)1 << 22 ? 32 : 8;
+    const int64_t lanes = 1 << std::min(5, log2_ceil(dim / 8));
+    const int64_t slices = (dim / 8 + lanes - 1) / lanes;
+    int r = 64 / copies;
+    while (r > 4 && n / r * slices * lanes < (int64_t)device_sm_count() * 4 * 768) r /= 2;
+    return r;
 }
 
 cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
@@ -1289,10 +1551,14 @@ cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
     a.slices = (a.dim / 8 + a.lanes - 1) / a.lanes;
     const int64_t chunks = (n + a.rows_per_chunk - 1) / a.rows_per_chunk;
     const int64_t threads = chunks * a.slices * a.lanes;
-    cudaError_t e = pdl_launch(k_embed_sum, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
+    auto f = a.copies == 1   ? k_embed_sum<1>
+             : a.copies == 2 ? k_embed_sum<2>
+             : a.copies <= 4 ? k_embed_sum<4>
+                             : k_embed_sum<8>;
+    cudaError_t e = pdl_launch(f, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
     if (e != cudaSuccess || chunks < 2) return e;
-    return pdl_launch(k_embed_join, dim3((unsigned)(chunks - 1), (unsigned)((a.dim + 255) / 256)),
-                      dim3(256), 0, s, a);
+    return pdl_launch(k_embed_join, dim3((unsigned)((chunks + 6) / 8), (unsigned)((a.dim + 255) / 256)),
+                      dim3(256), 0, s, a, chunks);
 }
 
 cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t s) {

@@ -474,7 +474,7 @@ engram_status engram_gate_bf16kv(const engram_ctx* ctx, int layer, const uint16_
  * [n][copies][dim], rounded once.  ENGRAM_MASKED gives zeros; any other id >=
  * rows gives zeros and sets the error word (ENGRAM_EBOUNDS at the next
  * engram_sync).  dim: a multiple of 8 up to 65,536; copies 1..8; rows up to
- * 2^32 - 2; n up to 2^30.  d_table and d_out 16-byte aligned. */
+ * 2^32 - 2; n up to 2^30, n x copies below 2^32.  d_table and d_out 16-byte aligned. */
 #define ENGRAM_EMBED_F32 0
 #define ENGRAM_EMBED_BF16 1
 engram_status engram_embed(engram_ctx* ctx, const void* d_table, int table_format, uint64_t rows,
