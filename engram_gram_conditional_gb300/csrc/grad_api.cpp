@@ -10,18 +10,20 @@ using namespace engram;
 
 namespace {
 
-// Carves a workspace into 256-byte aligned parts; with a null base it only
-// counts bytes.
+// Carves a workspace into 256-byte aligned parts (the caller's pointer need only
+// be 16-byte aligned); with a null base it only counts bytes.
 struct Carver {
     uint8_t* base;
     size_t at = 0;
-    explicit Carver(void* p) : base(static_cast<uint8_t*>(p)) {}
+    explicit Carver(void* p)
+        : base(reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 255) & ~(uintptr_t)255)) {}
     template <class T>
     T* take(size_t n) {
         T* p = base ? reinterpret_cast<T*>(base + at) : nullptr;
         at = (at + n * sizeof(T) + 255) & ~(size_t)255;
         return p;
     }
+    size_t bytes() const { return at ? at + 240 : 0; }  // with what aligning the base may skip
 };
 
 // The current device, and the context's device word on it (a context that has
@@ -79,7 +81,7 @@ EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
     for (int copies = 1; copies <= 8; ++copies)
         chunks = std::max(chunks, ceil_div(n, embed_rows_per_chunk(n, (int)dim, copies)));
     w.partial = c.take<float>((size_t)chunks * 2 * dim);
-    w.bytes = c.at;
+    w.bytes = c.bytes();
     return w;
 }
 
@@ -109,7 +111,7 @@ size_t gate_backward_ws(GateTrain* a, void* p, int64_t T, int hc, int d) {
         a->factors = f;
         a->dw_part = part;
     }
-    return c.at;
+    return c.bytes();
 }
 
 engram_status gate_backward_call(const engram_ctx* ctx, GateTrain& a, int saved, void* ws,
@@ -130,7 +132,7 @@ engram_status gate_backward_call(const engram_ctx* ctx, GateTrain& a, int saved,
 // ---- products ----------------------------------------------------------------------------
 
 // One of the two gradient products of a launch.
-GradProblem product(int64_t M, int64_t N, int64_t reduce, bool a_mn, uint16_t* out) {
+GradProblem product(int64_t M, int64_t N, int64_t reduce, bool a_mn) {
     GradProblem q{};
     q.m_units = (int)ceil_div(M, 2 * kBM);
     q.n_tiles = (int)ceil_div(N, kBN);
@@ -140,7 +142,6 @@ GradProblem product(int64_t M, int64_t N, int64_t reduce, bool a_mn, uint16_t* o
     q.group_m = 8;
     q.M = M;
     q.N = N;
-    q.out = out;
     return q;
 }
 
@@ -197,27 +198,26 @@ struct LossBackWs {
     int splits;
     size_t bytes;
 };
-GradProblem loss_dx(int64_t T, uint32_t dim, int64_t piece, uint16_t* out) {
-    GradProblem q = product(T, dim, piece, false, out);
+GradProblem loss_dx(int64_t T, uint32_t dim, int64_t piece) {
+    GradProblem q = product(T, dim, piece, false);
     q.a_tiled = (int)(piece / 64);
     return q;
 }
-GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece, uint16_t* out) {
-    GradProblem q = product(cols, dim, T, true, out);
+GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece) {
+    GradProblem q = product(cols, dim, T, true);
     q.a_tiled = (int)(piece / 64);
     q.n_fast = 1;
     return q;
 }
 LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim) {
     const int64_t piece = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
-    const GradProblem dx = loss_dx(T, dim, piece, nullptr);
-    const GradProblem dh = loss_dhead(T, dim, piece, piece, nullptr);
+    const GradProblem dx = loss_dx(T, dim, piece), dh = loss_dhead(T, dim, piece, piece);
     LossBackWs w{};
     w.splits = long_splits(dx, &dh);
     Carver c(p);
     w.dz = c.take<uint16_t>((size_t)rows * piece);
     w.acc = c.take<float>(w.splits > 1 || piece < vocab ? (size_t)w.splits * T * dim : 0);
-    w.bytes = c.at;
+    w.bytes = c.bytes();
     return w;
 }
 
@@ -401,11 +401,13 @@ engram_status engram_gate_backward_checkpoint(const engram_ctx* ctx, int layer,
 
 size_t engram_project_backward_workspace_bytes(const engram_ctx* ctx, int64_t T) {
     if (!ctx || check_T(T) || T == 0) return 0;
-    const GradProblem demb = product(T, ctx->K, ctx->N, false, nullptr);
-    const GradProblem dw = product(ctx->N, ctx->K, T, true, nullptr);
+    const GradProblem demb = product(T, ctx->K, ctx->N, false);
+    const GradProblem dw = product(ctx->N, ctx->K, T, true);
     // with or without the other product the cut may differ: room for either
     const int splits = std::max(long_splits(demb, &dw), long_splits(demb, nullptr));
-    return splits > 1 ? (size_t)splits * T * ctx->K * sizeof(float) : 0;
+    Carver c(nullptr);
+    c.take<float>(splits > 1 ? (size_t)splits * T * ctx->K : 0);
+    return c.bytes();
 }
 
 engram_status engram_project_backward(const engram_ctx* ctx, int layer, const uint16_t* d_emb,
@@ -428,28 +430,30 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
     GradArgs a{};
     a.err = ctx->d_err;
     a.wait_limit_ns = ctx->wait_limit_ns;
-    CUtensorMap tm[4];
+    CUtensorMap tm[6];
     cudaError_t e = cudaSuccess;
     if (d_dwkv) {
-        a.pr[1] = product(N, K, T, true, d_dwkv);
+        a.pr[1] = product(N, K, T, true);
         a.pr[1].n_fast = 1;
         e = make_tma_16bit(&tm[2], d_dkv, T, N, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[3], d_emb, T, K, 64, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[5], d_dwkv, N, K, 32, false);
     }
     if (d_demb && e == cudaSuccess) {
-        a.pr[0] = product(T, K, N, false, d_demb);
+        a.pr[0] = product(T, K, N, false);
         a.pr[0].splits = long_splits(a.pr[0], d_dwkv ? &a.pr[1] : nullptr);
         if (a.pr[0].splits > 1) {
             if (!d_workspace) return fail(ENGRAM_EINVAL, "null workspace");
-            a.pr[0].acc = static_cast<float*>(d_workspace);
+            a.pr[0].acc = Carver(d_workspace).take<float>(1);
             a.pr[0].acc_write = 1;
         }
         e = make_tma_16bit(&tm[0], d_dkv, T, N, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], L.w.wkv, N, K, 64, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[4], d_demb, T, K, 32, false);
     }
     if (e != cudaSuccess) return cuda_fail(e, "project backward tensor maps");
-    if (!d_demb) tm[0] = tm[2], tm[1] = tm[3];
-    if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1];
+    if (!d_demb) tm[0] = tm[2], tm[1] = tm[3], tm[4] = tm[5];
+    if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1], tm[5] = tm[4];
     e = launch_grad_products(a, tm, s);
     if (e == cudaSuccess && a.pr[0].acc_write)
         e = launch_sum_splits(a.pr[0].acc, a.pr[0].splits, T * K, d_demb, s);
@@ -462,7 +466,7 @@ size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
     Carver c(nullptr);
     c.take<float2>((size_t)ceil_div(vocab, kBN) * 2 * T);
     c.take<float>(T);
-    return c.at;
+    return c.bytes();
 }
 
 engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
@@ -484,18 +488,18 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
     GradArgs a{};
     a.err = ctx->d_err;
     a.wait_limit_ns = ctx->wait_limit_ns;
-    a.pr[0] = product(T, n_tiles * (int64_t)kBN, dim, false, nullptr);
+    a.pr[0] = product(T, n_tiles * (int64_t)kBN, dim, false);
     a.pr[0].group_m = loss_group_m(dim);
     a.T = T;
     a.vocab = (int)vocab;
     a.labels = d_labels;
     a.zlabel = zlabel;
     a.part = part;
-    CUtensorMap tm[4];
+    CUtensorMap tm[6];
     cudaError_t e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
     if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
     if (e != cudaSuccess) return cuda_fail(e, "loss tensor maps");
-    tm[2] = tm[0], tm[3] = tm[1];
+    tm[2] = tm[4] = tm[5] = tm[0], tm[3] = tm[1];
     e = launch_grad_lse(a, tm, s);
     if (e == cudaSuccess)
         e = launch_loss_combine(part, n_tiles * 2, T, zlabel, d_labels, (int)vocab, d_loss, d_lse,
@@ -542,7 +546,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         GradArgs a{};
         a.err = ctx->d_err;
         a.wait_limit_ns = ctx->wait_limit_ns;
-        a.pr[0] = product(T, piece, dim, false, nullptr);
+        a.pr[0] = product(T, piece, dim, false);
         a.pr[0].group_m = loss_group_m(dim);
         a.T = T;
         a.v0 = v0;
@@ -551,31 +555,36 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         a.labels = d_labels;
         a.lse = d_lse;
         a.dloss = d_dloss;
-        a.dz = w.dz;
-        CUtensorMap tm[4];
+        const uint64_t dz_rows = (uint64_t)rows * piece / 64;
+        CUtensorMap tm[6];
         tm[0] = tm[2] = x_k;
         e = make_tma_16bit(&tm[1], head, vocab - v0, dim, kBM, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[4], w.dz, dz_rows, 64, 32, false);
         if (e != cudaSuccess) break;
-        tm[3] = tm[1];
+        tm[3] = tm[1], tm[5] = tm[4];
         if ((e = launch_grad_dz(a, tm, s)) != cudaSuccess) break;
         // dx += dz head, dhead = dz^T x
         GradArgs g{};
         g.err = ctx->d_err;
         g.wait_limit_ns = ctx->wait_limit_ns;
-        const uint64_t dz_rows = (uint64_t)rows * piece / 64;
         e = make_tma_16bit(&tm[0], w.dz, dz_rows, 64, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], head, vocab - v0, dim, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[2], w.dz, dz_rows, 64, 64, false);
+        if (e == cudaSuccess && d_dx) e = make_tma_16bit(&tm[4], d_dx, T, dim, 32, false);
+        if (e == cudaSuccess && d_dhead)
+            e = make_tma_16bit(&tm[5], d_dhead + v0 * dim, cols, dim, 32, false);
         if (e != cudaSuccess) break;
         tm[3] = x_mn;
+        if (!d_dx) tm[4] = tm[5];
+        if (!d_dhead) tm[5] = tm[4];
         if (d_dx) {
-            g.pr[0] = loss_dx(T, dim, piece, d_dx);
+            g.pr[0] = loss_dx(T, dim, piece);
             g.pr[0].splits = std::min(w.splits, g.pr[0].kb);
             g.pr[0].acc = w.acc;
             g.pr[0].acc_read = !first;
             g.pr[0].acc_write = !last || w.splits > 1;
         }
-        if (d_dhead) g.pr[1] = loss_dhead(T, dim, cols, piece, d_dhead + v0 * dim);
+        if (d_dhead) g.pr[1] = loss_dhead(T, dim, cols, piece);
         e = launch_grad_products(g, tm, s);
     }
     if (e == cudaSuccess && d_dx && w.splits > 1)

@@ -14,7 +14,7 @@ enum GradEpilogue : int {
     kGradOut = 2,  // a product's output
 };
 
-// One matrix product out [M][N] of a launch, reduced over kb blocks of 64.
+// One matrix product out [M][N] (BF16) of a launch, reduced over kb blocks of 64.
 struct GradProblem {
     int m_units, n_tiles;  // 256-row units, 256-column tiles
     int kb, splits;        // k-blocks; the reduction is cut into `splits` items
@@ -23,7 +23,6 @@ struct GradProblem {
     int a_tiled;           // A in 128 x 64 tiles: tiles per row of tiles (0: row-major)
     int n_fast, group_m;   // item order: N inner, or groups of group_m units with M inner
     int64_t M, N;          // bounds of the output; N a multiple of 8
-    uint16_t* out;         // bf16 [M][N]
     float* acc;            // fp32 [splits][M][N]; acc_read: added to, acc_write: the
     int acc_read, acc_write;  // result stays there instead of going to out
 };
@@ -41,11 +40,11 @@ struct GradArgs {
     const float* dloss;
     float* zlabel;
     float2* part;          // [2 n_tiles][T] (maximum, sum)
-    uint16_t* dz;
 };
 
 int grad_pairs();  // CTA pairs of a launch that fills the device
-// tm: A and B of problem 0, A and B of problem 1
+// tm: A and B of problem 0, A and B of problem 1, the outputs of problems 0 (for
+// launch_grad_dz: dz as [tiles x 128][64]) and 1, in boxes of 32 rows
 cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);

@@ -40,7 +40,13 @@ constexpr int kTmemCols = 2 * kBN;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kChunk = 64 * kBK * 2;      // 8 KB: 64 MN elements x 64 k of an MN-major tile
 
-constexpr int kOffBar = kStages * kStage;
+// Per epilogue warp: 32 rows x 64 BF16 of a tile on their way out, as a TMA
+// store's swizzled box (16-byte stores of a row per thread, straight to memory,
+// took 4.5 us per tile where the MMAs of a 384-long reduction take 1.6).
+constexpr int kOut = 32 * 64 * 2;
+
+constexpr int kOffOut = kStages * kStage;
+constexpr int kOffBar = kOffOut + kEpiWarps * kOut;
 constexpr int kNumBars = 2 * kStages + 4;
 constexpr int kOffTmem = kOffBar + kNumBars * 8;
 constexpr int kOffFlag = kOffTmem + 4;
@@ -60,6 +66,35 @@ __host__ __device__ constexpr uint32_t grad_idesc(bool a_mn, bool b_mn) {
 __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kChunk >> 4) << 16) |
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// A 64-column, 32-row box of shared memory to global memory; what lies outside
+// the tensor is not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     (uint64_t)map),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// Row `lane` of a warp's box, 16-byte piece j (of 8), 128-byte swizzled.
+__device__ __forceinline__ uint32_t out_piece(uint32_t box, int lane, int j) {
+    return box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4));
+}
+// 32 bytes at a time: a whole sector per thread.
+__device__ __forceinline__ void ld_global_v8(const float* p, float (&f)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_v8(float* p, const float (&f)[8]) {
+    asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(f[0]), "f"(f[1]), "f"(f[2]),
+                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "l"(p)
+                 : "memory");
 }
 
 // Work item i of pair p: problem, M unit, N tile and k-block range.
@@ -108,6 +143,7 @@ template <int kEpi, bool kBMn>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+       const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
        const __grid_constant__ GradArgs a) {
     const uint32_t rank = cluster_ctarank();
     const bool issuer = rank == 0u;
@@ -238,6 +274,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
         // ---- epilogue ----
         const int q4 = warp & 3, grp = warp >> 2;  // TMEM quadrant; columns [128 grp, 128 grp + 128)
         const int m = q4 * 32 + lane;
+        const uint32_t box = sbase + kOffOut + (uint32_t)(warp * kOut);
         for (int i = 0; i < n_items; ++i) {
             const Item w = get_item(a, pair, pairs, i);
             const GradProblem& q = a.pr[w.pr];
@@ -311,78 +348,96 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                 if (row < a.T)
                     a.part[((int64_t)w.nt * 2 + grp) * a.T + row] = make_float2(mx, sum);
             } else if constexpr (kEpi == kGradDz) {
-                // columns of this warp: two 64-wide chunks of the tiled dz
+                // this warp's columns are two 64-wide chunks of the tiled dz
                 const int64_t tb = 2 * w.mu + rank;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int half = 0; half < 2; ++half) {
+                    if (lane == 0) tma_store_wait_read();
                     __syncwarp();
-                    uint32_t r[32];
-                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
-                    tmem_wait_ld();
-                    const int lc = col0 + c * 32;           // column within the piece
-                    const int64_t v0 = a.v0 + lc;            // column within the vocabulary
-                    const int64_t rel = (int64_t)label - v0;
-                    uint32_t o[16];
+                    const int chunk = (col0 >> 6) + half;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float d[2];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(taddr + (uint32_t)(half * 64 + c * 32), r);
+                        tmem_wait_ld();
+                        const int64_t v0 = a.v0 + chunk * 64 + c * 32;  // column within the vocabulary
+                        const int64_t rel = (int64_t)label - v0;
+                        uint32_t o[16];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            // (z - lse first: exact where p is near 1)
-                            float p = exp2f((__uint_as_float(r[j + u]) - lse) * kLog2e);
-                            if (rel == j + u) p -= 1.f;
-                            d[u] = label >= 0 && v0 + j + u < a.vocab ? p * dl : 0.f;
+                        for (int j = 0; j < 32; j += 2) {
+                            float d[2];
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                // (z - lse first: exact where p is near 1)
+                                float p = exp2f((__uint_as_float(r[j + u]) - lse) * kLog2e);
+                                if (rel == j + u) p -= 1.f;
+                                d[u] = label >= 0 && v0 + j + u < a.vocab ? p * dl : 0.f;
+                            }
+                            o[j / 2] = bf16x2_pack_rn(d[0], d[1]);
                         }
-                        o[j / 2] = bf16x2_pack_rn(d[0], d[1]);
-                    }
-                    uint4* dst = reinterpret_cast<uint4*>(
-                        a.dz + ((tb * a.dz_chunks + (lc >> 6)) * 128 + m) * 64 + (lc & 63));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 4; ++j)
+                            st_shared_v4(out_piece(box, lane, c * 4 + j),
+                                         make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        tma_store_2d(&tmO0, box, 0, (int)(tb * a.dz_chunks + chunk) * 128 + q4 * 32);
                 }
             } else {
                 // a product's output: BF16, from this reduction alone or added to
                 // what earlier pieces left in fp32; or the fp32 sum of a split
                 const bool in = row < q.M;
                 float* accp = q.acc ? q.acc + ((int64_t)w.split * q.M + row) * q.N : nullptr;
+                const CUtensorMap* tmO = w.pr ? &tmO1 : &tmO0;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    __syncwarp();
-                    uint32_t r[32];
-                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
-                    tmem_wait_ld();
-                    const int64_t n = col0 + c * 32;
-                    if (!in) continue;
-                    // N is a multiple of 8: groups of eight columns are in or out whole
+                for (int half = 0; half < 2; ++half) {
+                    if (!q.acc_write) {
+                        if (lane == 0) tma_store_wait_read();
+                        __syncwarp();
+                    }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        if (n + j >= q.N) continue;
-                        float v[8];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(taddr + (uint32_t)(half * 64 + c * 32), r);
+                        tmem_wait_ld();
+                        const int64_t n = col0 + half * 64 + c * 32;
+                        // N is a multiple of 8: groups of eight columns are in or out whole
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(r[j + u]);
-                        if (q.acc_read) {
-                            const float4 x = *reinterpret_cast<const float4*>(accp + n + j);
-                            const float4 y = *reinterpret_cast<const float4*>(accp + n + j + 4);
-                            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-                        }
-                        if (q.acc_write) {
-                            *reinterpret_cast<float4*>(accp + n + j) = make_float4(v[0], v[1], v[2], v[3]);
-                            *reinterpret_cast<float4*>(accp + n + j + 4) =
-                                make_float4(v[4], v[5], v[6], v[7]);
-                        } else {
-                            *reinterpret_cast<uint4*>(q.out + row * q.N + n + j) =
-                                make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
-                                           bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
+                        for (int j = 0; j < 32; j += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(r[j + u]);
+                            if (q.acc && in && n + j < q.N) {
+                                if (q.acc_read) {
+                                    float x[8];
+                                    ld_global_v8(accp + n + j, x);
+#pragma unroll
+                                    for (int u = 0; u < 8; ++u) v[u] += x[u];
+                                }
+                                if (q.acc_write) st_global_v8(accp + n + j, v);
+                            }
+                            if (!q.acc_write)
+                                st_shared_v4(out_piece(box, lane, c * 4 + j / 8),
+                                             make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
+                                                        bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7])));
                         }
                     }
+                    if (!q.acc_write) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        const int64_t x = col0 + half * 64, y = row - lane;
+                        if (lane == 0 && x < q.N && y < q.M) tma_store_2d(tmO, box, (int)x, (int)y);
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_rank(tempty(acc), 0));
         }
+        if (kEpi != kGradLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncthreads();
@@ -542,7 +597,7 @@ cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], a);
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
 }
 
 }  // namespace
