@@ -206,7 +206,6 @@ GradProblem loss_dx(int64_t T, uint32_t dim, int64_t piece) {
 GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece) {
     GradProblem q = product(cols, dim, T, true);
     q.a_tiled = (int)(piece / 64);
-    q.n_fast = 1;
     return q;
 }
 LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim) {
@@ -434,7 +433,6 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
     cudaError_t e = cudaSuccess;
     if (d_dwkv) {
         a.pr[1] = product(N, K, T, true);
-        a.pr[1].n_fast = 1;
         e = make_tma_16bit(&tm[2], d_dkv, T, N, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[3], d_emb, T, K, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[5], d_dwkv, N, K, 32, false);

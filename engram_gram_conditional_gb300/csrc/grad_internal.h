@@ -6,8 +6,6 @@
 
 namespace engram {
 
-constexpr int kMaxPairs = 96;
-
 enum GradEpilogue : int {
     kGradLse = 0,  // softmax statistics of the logits
     kGradDz = 1,   // dz of a piece of the vocabulary, BF16, in 128 x 64 tiles
@@ -21,7 +19,7 @@ struct GradProblem {
     int items;             // m_units * n_tiles * splits (set by the launcher)
     int a_mn;              // A is stored with M contiguous
     int a_tiled;           // A in 128 x 64 tiles: tiles per row of tiles (0: row-major)
-    int n_fast, group_m;   // item order: N inner, or groups of group_m units with M inner
+    int group_m;           // item order: groups of group_m units, M inner
     int64_t M, N;          // bounds of the output; N a multiple of 8
     float* acc;            // fp32 [splits][M][N]; acc_read: added to, acc_write: the
     int acc_read, acc_write;  // result stays there instead of going to out
@@ -29,7 +27,7 @@ struct GradProblem {
 
 struct GradArgs {
     GradProblem pr[2];
-    int light_start[kMaxPairs + 1];  // items [start[p], start[p + 1]) of pr[1] are pair p's
+    int pairs_more, rounds_fewer;  // how the items are dealt (set by the launcher)
     uint32_t* err;
     long long wait_limit_ns;
     // softmax epilogues

@@ -102,9 +102,29 @@ struct Item {
     int pr, mu, nt, kb_lo, nkb, split;
 };
 
+// The long problem's items go round robin: pair p has items p, p + pairs, ...; so
+// the first `a.pairs_more` pairs may have one more than the others.  The short
+// problem's items follow in order of the rounds in which the pairs get to them:
+// in the first a.rounds_fewer rounds only the pairs with fewer long items take
+// one each, then all pairs do, so that the pairs end together and those that run
+// at the same time work on neighbouring tiles.
+__device__ __forceinline__ int short_index(const GradArgs& a, int p, int pairs, int i) {
+    const int fewer = pairs - a.pairs_more;
+    if (p < a.pairs_more) return a.rounds_fewer * fewer + i * pairs + p;
+    if (i < a.rounds_fewer) return i * fewer + (p - a.pairs_more);
+    return a.rounds_fewer * fewer + (i - a.rounds_fewer) * pairs + p;
+}
+
 __device__ __forceinline__ int item_count(const GradArgs& a, int p, int pairs) {
     const int nh = a.pr[0].items > p ? (a.pr[0].items - p + pairs - 1) / pairs : 0;
-    return nh + (a.light_start[p + 1] - a.light_start[p]);
+    const int L = a.pr[1].items, fewer = pairs - a.pairs_more;
+    if (L == 0) return nh;
+    // items of this pair with short_index < L
+    const int first = a.rounds_fewer * fewer;
+    const int all = L > first + p ? (L - first - p + pairs - 1) / pairs : 0;
+    if (p < a.pairs_more) return nh + all;
+    const int b = p - a.pairs_more, upto = min(L, first);
+    return nh + (upto > b ? (upto - b + fewer - 1) / fewer : 0) + all;
 }
 
 __device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, int i) {
@@ -116,23 +136,20 @@ __device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, in
         idx = p + i * pairs;
     } else {
         it.pr = 1;
-        idx = a.light_start[p] + (i - nh);
+        idx = short_index(a, p, pairs, i - nh);
     }
     const GradProblem& q = a.pr[it.pr];
     const int tiles = q.m_units * q.n_tiles;
     it.split = idx / tiles;
     idx -= it.split * tiles;
-    if (q.n_fast) {
-        it.mu = idx / q.n_tiles;
-        it.nt = idx - it.mu * q.n_tiles;
-    } else {  // groups of group_m units, M inner: the pairs in flight share B tiles in L2
-        const int per = q.group_m * q.n_tiles;
-        const int g = idx / per, first = g * q.group_m;
-        const int gm = min(q.group_m, q.m_units - first);
-        const int r = idx - g * per;
-        it.nt = r / gm;
-        it.mu = first + (r - it.nt * gm);
-    }
+    // groups of group_m units, M inner: the pairs in flight share tiles of both
+    // operands in L2
+    const int per = q.group_m * q.n_tiles;
+    const int g = idx / per, first = g * q.group_m;
+    const int gm = min(q.group_m, q.m_units - first);
+    const int r = idx - g * per;
+    it.nt = r / gm;
+    it.mu = first + (r - it.nt * gm);
     it.kb_lo = (int)((int64_t)it.split * q.kb / q.splits);
     it.nkb = (int)((int64_t)(it.split + 1) * q.kb / q.splits) - it.kb_lo;
     return it;
@@ -512,25 +529,15 @@ __global__ void k_sum_splits(const float* acc, int splits, int64_t n, uint16_t* 
                    bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
 }
 
-// The pairs' shares of the short problem: pair p has the k-blocks of its round-
-// robin items of the long one; each is filled up to the common mean.
+// How many rounds of short items fit into the time of one long item.
 void share_items(GradArgs& a, int pairs) {
-    auto cost = [](const GradProblem& q) { return q.items ? (double)q.kb / q.splits + 1.0 : 0.0; };
-    const double ch = cost(a.pr[0]), cl = cost(a.pr[1]);
-    const int H = a.pr[0].items, L = a.pr[1].items;
-    const double mean = (H * ch + L * cl) / pairs;
-    double want = 0;  // items the pairs so far should have taken
-    double total = 0;
-    auto room = [&](int p) {
-        const int nh = H > p ? (H - p + pairs - 1) / pairs : 0;
-        return std::max(0.0, mean - nh * ch);
-    };
-    for (int p = 0; p < pairs; ++p) total += room(p);
-    a.light_start[0] = 0;
-    for (int p = 0; p < pairs; ++p) {
-        want += total > 0 ? room(p) / total * L : (double)L / pairs;
-        a.light_start[p + 1] = p + 1 == pairs ? L : std::min(L, (int)std::floor(want + 0.5));
-    }
+    a.pairs_more = a.pr[0].items % pairs;
+    a.rounds_fewer = 0;
+    if (!a.pr[0].items || !a.pr[1].items || !a.pairs_more) return;
+    // an item takes its k-blocks, but no less than writing out a tile (about 6)
+    auto cost = [](const GradProblem& q) { return std::max(6.0, (double)q.kb / q.splits) + 0.5; };
+    const int fewer = pairs - a.pairs_more;
+    a.rounds_fewer = std::min((int)(cost(a.pr[0]) / cost(a.pr[1]) + 0.5), (a.pr[1].items + fewer - 1) / fewer);
 }
 
 cudaError_t pdl_launch(void* f, dim3 grid, dim3 block, void** args, cudaStream_t s) {
@@ -570,7 +577,7 @@ cudaError_t resident_pairs(int* pairs) {
         e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorLaunchOutOfResources;
-        known = std::min(std::min(n, device_sm_count() / 2), kMaxPairs);
+        known = std::min(n, device_sm_count() / 2);
     }
     *pairs = known;
     return cudaSuccess;
@@ -602,7 +609,7 @@ cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
 
 }  // namespace
 
-int grad_pairs() { return std::min(device_sm_count() / 2, kMaxPairs); }
+int grad_pairs() { return device_sm_count() / 2; }
 
 cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
     return launch<kGradLse, false>(a, tm, s);
