@@ -429,16 +429,17 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
     GradArgs a{};
     a.err = ctx->d_err;
     a.wait_limit_ns = ctx->wait_limit_ns;
-    CUtensorMap tm[6];
+    CUtensorMap tm[4];
     cudaError_t e = cudaSuccess;
     if (d_dwkv) {
         a.pr[1] = product(N, K, T, true);
+        a.pr[1].out = d_dwkv;
         e = make_tma_16bit(&tm[2], d_dkv, T, N, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[3], d_emb, T, K, 64, false);
-        if (e == cudaSuccess) e = make_tma_16bit(&tm[5], d_dwkv, N, K, 32, false);
     }
     if (d_demb && e == cudaSuccess) {
         a.pr[0] = product(T, K, N, false);
+        a.pr[0].out = d_demb;
         a.pr[0].splits = long_splits(a.pr[0], d_dwkv ? &a.pr[1] : nullptr);
         if (a.pr[0].splits > 1) {
             if (!d_workspace) return fail(ENGRAM_EINVAL, "null workspace");
@@ -447,11 +448,10 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
         }
         e = make_tma_16bit(&tm[0], d_dkv, T, N, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], L.w.wkv, N, K, 64, false);
-        if (e == cudaSuccess) e = make_tma_16bit(&tm[4], d_demb, T, K, 32, false);
     }
     if (e != cudaSuccess) return cuda_fail(e, "project backward tensor maps");
-    if (!d_demb) tm[0] = tm[2], tm[1] = tm[3], tm[4] = tm[5];
-    if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1], tm[5] = tm[4];
+    if (!d_demb) tm[0] = tm[2], tm[1] = tm[3];
+    if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1];
     e = launch_grad_products(a, tm, s);
     if (e == cudaSuccess && a.pr[0].acc_write)
         e = launch_sum_splits(a.pr[0].acc, a.pr[0].splits, T * K, d_demb, s);
@@ -493,11 +493,11 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
     a.labels = d_labels;
     a.zlabel = zlabel;
     a.part = part;
-    CUtensorMap tm[6];
+    CUtensorMap tm[4];
     cudaError_t e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
     if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
     if (e != cudaSuccess) return cuda_fail(e, "loss tensor maps");
-    tm[2] = tm[4] = tm[5] = tm[0], tm[3] = tm[1];
+    tm[2] = tm[0], tm[3] = tm[1];
     e = launch_grad_lse(a, tm, s);
     if (e == cudaSuccess)
         e = launch_loss_combine(part, n_tiles * 2, T, zlabel, d_labels, (int)vocab, d_loss, d_lse,
@@ -553,36 +553,35 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         a.labels = d_labels;
         a.lse = d_lse;
         a.dloss = d_dloss;
-        const uint64_t dz_rows = (uint64_t)rows * piece / 64;
-        CUtensorMap tm[6];
+        a.dz = w.dz;
+        CUtensorMap tm[4];
         tm[0] = tm[2] = x_k;
         e = make_tma_16bit(&tm[1], head, vocab - v0, dim, kBM, false);
-        if (e == cudaSuccess) e = make_tma_16bit(&tm[4], w.dz, dz_rows, 64, 32, false);
         if (e != cudaSuccess) break;
-        tm[3] = tm[1], tm[5] = tm[4];
+        tm[3] = tm[1];
         if ((e = launch_grad_dz(a, tm, s)) != cudaSuccess) break;
         // dx += dz head, dhead = dz^T x
         GradArgs g{};
         g.err = ctx->d_err;
         g.wait_limit_ns = ctx->wait_limit_ns;
+        const uint64_t dz_rows = (uint64_t)rows * piece / 64;
         e = make_tma_16bit(&tm[0], w.dz, dz_rows, 64, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], head, vocab - v0, dim, 64, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[2], w.dz, dz_rows, 64, 64, false);
-        if (e == cudaSuccess && d_dx) e = make_tma_16bit(&tm[4], d_dx, T, dim, 32, false);
-        if (e == cudaSuccess && d_dhead)
-            e = make_tma_16bit(&tm[5], d_dhead + v0 * dim, cols, dim, 32, false);
         if (e != cudaSuccess) break;
         tm[3] = x_mn;
-        if (!d_dx) tm[4] = tm[5];
-        if (!d_dhead) tm[5] = tm[4];
         if (d_dx) {
             g.pr[0] = loss_dx(T, dim, piece);
+            g.pr[0].out = d_dx;
             g.pr[0].splits = std::min(w.splits, g.pr[0].kb);
             g.pr[0].acc = w.acc;
             g.pr[0].acc_read = !first;
             g.pr[0].acc_write = !last || w.splits > 1;
         }
-        if (d_dhead) g.pr[1] = loss_dhead(T, dim, cols, piece);
+        if (d_dhead) {
+            g.pr[1] = loss_dhead(T, dim, cols, piece);
+            g.pr[1].out = d_dhead + v0 * dim;
+        }
         e = launch_grad_products(g, tm, s);
     }
     if (e == cudaSuccess && d_dx && w.splits > 1)

@@ -12,6 +12,10 @@ enum GradEpilogue : int {
     kGradOut = 2,  // a product's output
 };
 
+struct FastDiv {
+    uint32_t d, m, s;  // divisor, multiplier, shift
+};
+
 // One matrix product out [M][N] (BF16) of a launch, reduced over kb blocks of 64.
 struct GradProblem {
     int m_units, n_tiles;  // 256-row units, 256-column tiles
@@ -20,7 +24,9 @@ struct GradProblem {
     int a_mn;              // A is stored with M contiguous
     int a_tiled;           // A in 128 x 64 tiles: tiles per row of tiles (0: row-major)
     int group_m;           // item order: groups of group_m units, M inner
+    FastDiv per_split, per_group, in_group, in_last;  // (set by the launcher)
     int64_t M, N;          // bounds of the output; N a multiple of 8
+    uint16_t* out;         // bf16 [M][N]
     float* acc;            // fp32 [splits][M][N]; acc_read: added to, acc_write: the
     int acc_read, acc_write;  // result stays there instead of going to out
 };
@@ -38,11 +44,11 @@ struct GradArgs {
     const float* dloss;
     float* zlabel;
     float2* part;          // [2 n_tiles][T] (maximum, sum)
+    uint16_t* dz;          // 128 x 64 tiles [row block][64-column chunk of the piece]
 };
 
 int grad_pairs();  // CTA pairs of a launch that fills the device
-// tm: A and B of problem 0, A and B of problem 1, the outputs of problems 0 (for
-// launch_grad_dz: dz as [tiles x 128][64]) and 1, in boxes of 32 rows
+// tm: A and B of problem 0, A and B of problem 1
 cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);

@@ -33,25 +33,35 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kCols = kBN / (kEpiWarps / 4);  // of a tile, per epilogue warp
 constexpr int kOperand = kBM * kBK * 2;   // 16 KB: one CTA's A or B of a stage
 constexpr int kStage = 2 * kOperand;
-constexpr int kStages = 6;
 constexpr int kTmemCols = 2 * kBN;
+// k-blocks that the loss's logits sum in one accumulator.  The tensor core's
+// additions to an accumulator truncate: over 5,120 products that took 1.5e-6 off
+// a loss (relative; 1e-7 with sums rounded to nearest).  So the epilogue takes
+// the accumulator every 1,024 products and adds it in registers.
+constexpr int kLseSegment = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kChunk = 64 * kBK * 2;      // 8 KB: 64 MN elements x 64 k of an MN-major tile
+// An epilogue warp turns 32 rows x 64 BF16 of a tile from a row per lane into
+// whole 128-byte lines through a box of shared memory.  (16-byte stores of a row
+// per lane, straight to memory, took 4.5 us per tile where the MMAs of a
+// 384-long reduction take 1.6.)
+constexpr int kBox = 32 * 64 * 2;
 
-// Per epilogue warp: 32 rows x 64 BF16 of a tile on their way out, as a TMA
-// store's swizzled box (16-byte stores of a row per thread, straight to memory,
-// took 4.5 us per tile where the MMAs of a 384-long reduction take 1.6).
-constexpr int kOut = 32 * 64 * 2;
-
-constexpr int kOffOut = kStages * kStage;
-constexpr int kOffBar = kOffOut + kEpiWarps * kOut;
-constexpr int kNumBars = 2 * kStages + 4;
-constexpr int kOffTmem = kOffBar + kNumBars * 8;
-constexpr int kOffFlag = kOffTmem + 4;
-constexpr int kSmem = kOffFlag + 4 + 1024;
-static_assert(kSmem <= 232448, "shared memory above the per-block limit");
+// Shared memory of each variant.
+template <int kEpi>
+struct Layout {
+    static constexpr int kStages = kEpi == kGradLse ? 7 : 6;
+    static constexpr int kOffOut = kStages * kStage;
+    static constexpr int kOffBar = kOffOut + (kEpi == kGradLse ? 0 : kEpiWarps * kBox);
+    static constexpr int kNumBars = 2 * kStages + 4;
+    static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+    static constexpr int kOffFlag = kOffTmem + 4;
+    static constexpr int kSmem = kOffFlag + 4 + 1024;
+    static_assert(kSmem <= 232448, "shared memory above the per-block limit");
+};
 
 // Instruction descriptor, kind::f16, BF16 operands, fp32 accumulate, M = 256
 // (a pair), N = 256; bit 15 / 16: A / B is MN-major.
@@ -68,21 +78,26 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// A 64-column, 32-row box of shared memory to global memory; what lies outside
-// the tensor is not written.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     (uint64_t)map),
-                 "r"(src), "r"(x), "r"(y)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+// Row r of a warp's box, 16-byte piece j (of 8), swizzled against bank conflicts.
+__device__ __forceinline__ uint32_t out_piece(uint32_t box, int r, int j) {
+    return box + (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ void tma_store_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// Row `lane` of a warp's box, 16-byte piece j (of 8), 128-byte swizzled.
-__device__ __forceinline__ uint32_t out_piece(uint32_t box, int lane, int j) {
-    return box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4));
+// The box to memory, four rows per instruction: rows `ld` elements apart from
+// `dst`, of which the first `rows` and the first `cols` columns (a multiple of 8)
+// are written.
+__device__ __forceinline__ void put_box(uint32_t box, int lane, uint16_t* dst, int64_t ld, int64_t rows,
+                                        int64_t cols) {
+    const int j = lane & 7;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + (lane >> 3);
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(out_piece(box, r, j))
+                     : "memory");
+        if (r < rows && 8 * j < cols) *reinterpret_cast<uint4*>(dst + r * ld + 8 * j) = v;
+    }
 }
 // 32 bytes at a time: a whole sector per thread.
 __device__ __forceinline__ void ld_global_v8(const float* p, float (&f)[8]) {
@@ -127,31 +142,38 @@ __device__ __forceinline__ int item_count(const GradArgs& a, int p, int pairs) {
     return nh + (upto > b ? (upto - b + fewer - 1) / fewer : 0) + all;
 }
 
-__device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, int i) {
-    const int nh = a.pr[0].items > p ? (a.pr[0].items - p + pairs - 1) / pairs : 0;
+// n / d for n < 2^31 (see fast_div on the host).
+__device__ __forceinline__ int divide(int n, const FastDiv& d) {
+    return d.d == 1 ? n : (int)(__umulhi((uint32_t)n, d.m) >> d.s);
+}
+
+__device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, int n_long, int i) {
     Item it;
     int idx;
-    if (i < nh) {
+    if (i < n_long) {
         it.pr = 0;
         idx = p + i * pairs;
     } else {
         it.pr = 1;
-        idx = short_index(a, p, pairs, i - nh);
+        idx = short_index(a, p, pairs, i - n_long);
     }
     const GradProblem& q = a.pr[it.pr];
-    const int tiles = q.m_units * q.n_tiles;
-    it.split = idx / tiles;
-    idx -= it.split * tiles;
+    it.split = 0;
+    it.kb_lo = 0;
+    it.nkb = q.kb;
+    if (q.splits > 1) {
+        it.split = divide(idx, q.per_split);
+        idx -= it.split * (int)q.per_split.d;
+        it.kb_lo = it.split * q.kb / q.splits;
+        it.nkb = (it.split + 1) * q.kb / q.splits - it.kb_lo;
+    }
     // groups of group_m units, M inner: the pairs in flight share tiles of both
     // operands in L2
-    const int per = q.group_m * q.n_tiles;
-    const int g = idx / per, first = g * q.group_m;
-    const int gm = min(q.group_m, q.m_units - first);
-    const int r = idx - g * per;
-    it.nt = r / gm;
-    it.mu = first + (r - it.nt * gm);
-    it.kb_lo = (int)((int64_t)it.split * q.kb / q.splits);
-    it.nkb = (int)((int64_t)(it.split + 1) * q.kb / q.splits) - it.kb_lo;
+    const int g = divide(idx, q.per_group), first = g * q.group_m;
+    const int r = idx - g * (int)q.per_group.d;
+    const FastDiv& gm = first + q.group_m <= q.m_units ? q.in_group : q.in_last;
+    it.nt = divide(r, gm);
+    it.mu = first + (r - it.nt * (int)gm.d);
     return it;
 }
 
@@ -160,8 +182,10 @@ template <int kEpi, bool kBMn>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-       const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
        const __grid_constant__ GradArgs a) {
+    using L = Layout<kEpi>;
+    constexpr int kSegment = kEpi == kGradLse ? kLseSegment : 1 << 30;
+    constexpr int kStages = L::kStages, kOffBar = L::kOffBar;
     const uint32_t rank = cluster_ctarank();
     const bool issuer = rank == 0u;
     extern __shared__ uint8_t smem_dyn[];
@@ -173,8 +197,8 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
     auto empty = [&](int s) { return sbase + kOffBar + 8u * (uint32_t)(kStages + s); };
     auto tfull = [&](int acc) { return sbase + kOffBar + 8u * (uint32_t)(2 * kStages + acc); };
     auto tempty = [&](int acc) { return sbase + kOffBar + 8u * (uint32_t)(2 * kStages + 2 + acc); };
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffFlag);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffFlag);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffTmem);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -199,6 +223,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
 
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
     const int n_items = item_count(a, pair, pairs);
+    const int n_long = a.pr[0].items > pair ? (a.pr[0].items - pair + pairs - 1) / pairs : 0;
     const long long lim = a.wait_limit_ns;
     auto fail = [&]() {
         *abort_flag = 1;
@@ -210,7 +235,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
             int it = 0;
             bool ok = true;
             for (int i = 0; i < n_items && ok; ++i) {
-                const Item w = get_item(a, pair, pairs, i);
+                const Item w = get_item(a, pair, pairs, n_long, i);
                 const GradProblem& q = a.pr[w.pr];
                 const CUtensorMap* tmA = w.pr ? &tmA1 : &tmA0;
                 const CUtensorMap* tmB = w.pr ? &tmB1 : &tmB0;
@@ -252,23 +277,29 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
         }
     } else if (warp == kWarpMma) {
         if (lane == 0 && issuer) {
-            int it = 0;
+            int it = 0, use = 0;  // stages, accumulators used so far
             bool ok = true;
             for (int i = 0; i < n_items && ok; ++i) {
-                const int acc = i & 1;
-                if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(i >> 1) & 1u) ^ 1u, abort_flag, lim)) {
-                    fail();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
-                const Item w = get_item(a, pair, pairs, i);
-                const bool a_mn = a.pr[w.pr].a_mn != 0;
+                const GradProblem& q = a.pr[i < n_long ? 0 : 1];
+                const int nkb = q.splits > 1 ? get_item(a, pair, pairs, n_long, i).nkb : q.kb;
+                const bool a_mn = q.a_mn != 0;
                 const uint32_t id = grad_idesc(a_mn, kBMn);
                 // 16 of the reduction: 32 bytes of a K-major row, or 16 rows of 128 bytes
                 const uint64_t a_step = a_mn ? 128ull : 2ull, b_step = kBMn ? 128ull : 2ull;
-                for (int j = 0; j < w.nkb; ++j, ++it) {
+                uint32_t d_tmem = 0;
+                int seg = 0;  // k-blocks in the current accumulator
+                for (int j = 0; j < nkb; ++j, ++it) {
                     const int s = it % kStages;
+                    if (seg == 0) {
+                        const int acc = use & 1;
+                        if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(use >> 1) & 1u) ^ 1u, abort_flag, lim)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        d_tmem = tmem_base + (uint32_t)(acc * kBN);
+                    }
                     if (!mbar_wait_cluster(full(s), (uint32_t)(it / kStages) & 1u, abort_flag, lim)) {
                         fail();
                         ok = false;
@@ -281,25 +312,45 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
                         umma_f16kind_pair(d_tmem, ad + a_step * k, bd + b_step * k, id,
-                                          (j != 0) || (k != 0));
+                                          (seg != 0) || (k != 0));
                     umma_commit_pair(empty(s));
+                    if (++seg == kSegment || j + 1 == nkb) {
+                        umma_commit_pair(tfull(use & 1));
+                        ++use;
+                        seg = 0;
+                    }
                 }
-                if (ok) umma_commit_pair(tfull(acc));
             }
         }
     } else {
         // ---- epilogue ----
-        const int q4 = warp & 3, grp = warp >> 2;  // TMEM quadrant; columns [128 grp, 128 grp + 128)
+        const int q4 = warp & 3, grp = warp >> 2;  // TMEM quadrant; columns [kCols grp, kCols grp + kCols)
         const int m = q4 * 32 + lane;
-        const uint32_t box = sbase + kOffOut + (uint32_t)(warp * kOut);
+        const uint32_t box = sbase + L::kOffOut + (uint32_t)(warp * kBox);
+        int use = 0;  // accumulators used so far
+        auto acc_ready = [&]() {
+            const int acc = use & 1;
+            int ready = 1;
+            if (lane == 0) ready = mbar_wait_cluster(tfull(acc), (uint32_t)(use >> 1) & 1u, abort_flag, lim);
+            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
+            if (!ready && lane == 0) fail();
+            tc_fence_after();
+            return ready != 0;
+        };
+        auto acc_done = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(tempty(use & 1), 0));
+            ++use;
+        };
         for (int i = 0; i < n_items; ++i) {
-            const Item w = get_item(a, pair, pairs, i);
+            const Item w = get_item(a, pair, pairs, n_long, i);
             const GradProblem& q = a.pr[w.pr];
-            const int acc = i & 1;
             const int64_t row = ((int64_t)2 * w.mu + rank) * kBM + m;
-            const int col0 = w.nt * kBN + grp * 128;
-            const uint32_t taddr = tmem_base + (uint32_t)(acc * kBN + grp * 128) +
-                                   ((uint32_t)(q4 * 32) << 16);
+            const int col0 = w.nt * kBN + grp * kCols;
+            auto acc_addr = [&]() {
+                return tmem_base + (uint32_t)((use & 1) * kBN + grp * kCols) + ((uint32_t)(q4 * 32) << 16);
+            };
             float lse = 0.f, dl = 0.f;
             int label = -1;
             if (kEpi == kGradLse || kEpi == kGradDz) {
@@ -312,65 +363,69 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                     }
                 }
             }
-            int ready = 1;
-            if (lane == 0) ready = mbar_wait_cluster(tfull(acc), (uint32_t)(i >> 1) & 1u, abort_flag, lim);
-            ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
-            if (!ready) {
-                if (lane == 0) fail();
-                break;
-            }
-            tc_fence_after();
             if constexpr (kEpi == kGradLse) {
+                float v[4][32];
+                bool ok = true;
+                for (int seg = 0; seg < w.nkb && ok; seg += kSegment) {
+                    ok = acc_ready();
+                    const uint32_t taddr = acc_addr();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(taddr + (uint32_t)(c * 32), r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[c][j] = seg ? v[c][j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+                    }
+                    acc_done();
+                }
+                if (!ok) break;
                 // running maximum and sum over this warp's 128 columns
                 float mx = -INFINITY, sum = 0.f;
                 const int64_t zrel = (int64_t)label - col0;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    __syncwarp();
-                    uint32_t r[32];
-                    tmem_ld32(taddr + (uint32_t)(c * 32), r);
-                    tmem_wait_ld();
-                    float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                for (int c = 0; c < 4; ++c) {
                     if (label >= 0 && zrel >= c * 32 && zrel < c * 32 + 32) {
                         float z = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (zrel == c * 32 + j) z = v[j];
+                            if (zrel == c * 32 + j) z = v[c][j];
                         a.zlabel[row] = z;
                     }
                     const int lastc = a.vocab - (col0 + c * 32);
                     if (lastc < 32) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j >= lastc) v[j] = -INFINITY;
+                            if (j >= lastc) v[c][j] = -INFINITY;
                     }
-                    float cm = v[0];
-                    bool nan = v[0] != v[0];
+                    float cm = v[c][0];
+                    bool nan = v[c][0] != v[c][0];
 #pragma unroll
                     for (int j = 1; j < 32; ++j) {
-                        nan |= v[j] != v[j];
-                        cm = fmaxf(cm, v[j]);
+                        nan |= v[c][j] != v[c][j];
+                        cm = fmaxf(cm, v[c][j]);
                     }
                     const float nm = fmaxf(mx, cm);
                     const float base = nm == -INFINITY ? 0.f : nm;
                     float cs = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) cs += exp2f((v[j] - base) * kLog2e);
+                    for (int j = 0; j < 32; ++j) cs += exp2f((v[c][j] - base) * kLog2e);
                     sum = sum * exp2f((mx - base) * kLog2e) + cs;
                     if (nan) sum = NAN;
                     mx = nm;
                 }
                 if (row < a.T)
                     a.part[((int64_t)w.nt * 2 + grp) * a.T + row] = make_float2(mx, sum);
-            } else if constexpr (kEpi == kGradDz) {
+                continue;
+            }
+            if (!acc_ready()) break;
+            const uint32_t taddr = acc_addr();
+            if constexpr (kEpi == kGradDz) {
                 // this warp's columns are two 64-wide chunks of the tiled dz
                 const int64_t tb = 2 * w.mu + rank;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    if (lane == 0) tma_store_wait_read();
-                    __syncwarp();
                     const int chunk = (col0 >> 6) + half;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -397,23 +452,49 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                             st_shared_v4(out_piece(box, lane, c * 4 + j),
                                          make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
                     }
-                    fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0)
-                        tma_store_2d(&tmO0, box, 0, (int)(tb * a.dz_chunks + chunk) * 128 + q4 * 32);
+                    put_box(box, lane, a.dz + ((tb * a.dz_chunks + chunk) * 128 + q4 * 32) * 64, 64, 32, 64);
+                    __syncwarp();
                 }
-            } else {
-                // a product's output: BF16, from this reduction alone or added to
-                // what earlier pieces left in fp32; or the fp32 sum of a split
-                const bool in = row < q.M;
-                float* accp = q.acc ? q.acc + ((int64_t)w.split * q.M + row) * q.N : nullptr;
-                const CUtensorMap* tmO = w.pr ? &tmO1 : &tmO0;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    if (!q.acc_write) {
-                        if (lane == 0) tma_store_wait_read();
+            } else if constexpr (kEpi == kGradOut) {
+                if (!q.acc) {
+                    // the accumulator is handed back before the first store: the
+                    // arrival is a release, which waits for the stores before it
+                    // (1,200 to 2,600 cycles)
+                    uint32_t o[4][16];
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2) {
+                        uint32_t r[2][32];
+                        tmem_ld32(taddr + (uint32_t)(c * 32), r[0]);
+                        tmem_ld32(taddr + (uint32_t)(c * 32 + 32), r[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[c + j / 16][j % 16] =
+                                bf16x2_pack_rn(__uint_as_float(r[j / 16][2 * (j % 16)]),
+                                               __uint_as_float(r[j / 16][2 * (j % 16) + 1]));
+                    }
+                    acc_done();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t* p = o[2 * half + j / 4] + 4 * (j % 4);
+                            st_shared_v4(out_piece(box, lane, j), make_uint4(p[0], p[1], p[2], p[3]));
+                        }
+                        __syncwarp();
+                        const int64_t x = col0 + half * 64, y = row - lane;
+                        put_box(box, lane, q.out + y * q.N + x, q.N, q.M - y, q.N - x);
                         __syncwarp();
                     }
+                    continue;
+                }
+                // added to what earlier pieces left in fp32; out as BF16 from the
+                // last piece, else (and from a split) as fp32
+                const bool in = row < q.M;
+                float* accp = q.acc + ((int64_t)w.split * q.M + row) * q.N;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t r[32];
@@ -426,7 +507,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                             float v[8];
 #pragma unroll
                             for (int u = 0; u < 8; ++u) v[u] = __uint_as_float(r[j + u]);
-                            if (q.acc && in && n + j < q.N) {
+                            if (in && n + j < q.N) {
                                 if (q.acc_read) {
                                     float x[8];
                                     ld_global_v8(accp + n + j, x);
@@ -441,20 +522,16 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                                                         bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7])));
                         }
                     }
-                    if (!q.acc_write) {
-                        fence_proxy_async();
-                        __syncwarp();
-                        const int64_t x = col0 + half * 64, y = row - lane;
-                        if (lane == 0 && x < q.N && y < q.M) tma_store_2d(tmO, box, (int)x, (int)y);
-                    }
                     __syncwarp();
+                    if (!q.acc_write) {
+                        const int64_t x = col0 + half * 64, y = row - lane;
+                        put_box(box, lane, q.out + y * q.N + x, q.N, q.M - y, q.N - x);
+                        __syncwarp();
+                    }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(tempty(acc), 0));
+            acc_done();
         }
-        if (kEpi != kGradLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncthreads();
@@ -529,13 +606,32 @@ __global__ void k_sum_splits(const float* acc, int splits, int64_t n, uint16_t* 
                    bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
 }
 
+// q = floor(n / d) = floor(n m / 2^(31 + l)) for n < 2^31, with l = ceil(log2 d)
+// and m = ceil(2^(31 + l) / d): the excess m d - 2^(31 + l) < d <= 2^l, times n,
+// stays below 2^(31 + l).  (Granlund and Montgomery, PLDI 1994.)
+FastDiv fast_div(int d) {
+    int l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    FastDiv f{};
+    f.d = (uint32_t)d;
+    if (d > 1) {
+        f.m = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint32_t)d - 1) / (uint32_t)d);
+        f.s = (uint32_t)(l - 1);
+    }
+    return f;
+}
+
 // How many rounds of short items fit into the time of one long item.
 void share_items(GradArgs& a, int pairs) {
     a.pairs_more = a.pr[0].items % pairs;
     a.rounds_fewer = 0;
     if (!a.pr[0].items || !a.pr[1].items || !a.pairs_more) return;
-    // an item takes its k-blocks, but no less than writing out a tile (about 6)
-    auto cost = [](const GradProblem& q) { return std::max(6.0, (double)q.kb / q.splits) + 0.5; };
+    // an item takes its k-blocks and a little; a short one what writing out its
+    // tile takes (measured: 11 k-blocks' time at one k-block, 14 at six, 34 at 32)
+    auto cost = [](const GradProblem& q) {
+        const double kb = (double)q.kb / q.splits;
+        return std::max(kb + 2.0, 11.0 + 0.5 * kb);
+    };
     const int fewer = pairs - a.pairs_more;
     a.rounds_fewer = std::min((int)(cost(a.pr[0]) / cost(a.pr[1]) + 0.5), (a.pr[1].items + fewer - 1) / fewer);
 }
@@ -560,7 +656,8 @@ cudaError_t resident_pairs(int* pairs) {
     static int known = 0;
     if (!known) {
         auto kern = k_grad<kEpi, kBMn>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Layout<kEpi>::kSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -570,7 +667,7 @@ cudaError_t resident_pairs(int* pairs) {
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(2 * (device_sm_count() / 2));
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
+        cfg.dynamicSmemBytes = Layout<kEpi>::kSmem;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
@@ -586,7 +683,14 @@ cudaError_t resident_pairs(int* pairs) {
 template <int kEpi, bool kBMn>
 cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
     auto kern = k_grad<kEpi, kBMn>;
-    for (GradProblem& q : a.pr) q.items = q.m_units * q.n_tiles * q.splits;
+    for (GradProblem& q : a.pr) {
+        q.items = q.m_units * q.n_tiles * q.splits;
+        if (!q.items) continue;
+        q.per_split = fast_div(q.m_units * q.n_tiles);
+        q.per_group = fast_div(q.group_m * q.n_tiles);
+        q.in_group = fast_div(q.group_m);
+        q.in_last = fast_div(q.m_units % q.group_m ? q.m_units % q.group_m : q.group_m);
+    }
     const int total = a.pr[0].items + a.pr[1].items;
     if (!total) return cudaSuccess;
     int pairs = 0;
@@ -600,11 +704,11 @@ cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = Layout<kEpi>::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a);
+    return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], a);
 }
 
 }  // namespace
