@@ -733,7 +733,7 @@ __device__ __forceinline__ void block_sum(float (&v)[kN], float (*sm)[kN]) {
     }
 }
 
-// ---- gate with checkpoint ------------------------------------------------------------------
+// ---- gate with checkpoint: geometries whose tokens do not fit the one-pass kernel ---------------
 // One block per token: per branch, the sums of h^2, k^2 and h w k while h and k
 // are packed into the checkpoint; then hidden_out = h + g v for every branch
 // from one read of v (h comes from L2 the second time).
@@ -1271,46 +1271,250 @@ k_gate_backward_fused(const GateTrain a, int stages, int cs) {
     if (cs > 1) cluster_sync();  // no arrival may target a CTA that exited
 }
 
-// Cluster size and stages of the fused kernel for a geometry; 0 if none holds
-// three stages of a token (one in each phase and one on its way).
-template <int kSaved>
-int fused_cluster(int hc, int d, int* stages) {
-    const int groups = d / 256;
-    for (int cs = 1; cs <= 8 && cs <= groups; cs *= 2) {
-        const int per = (groups + cs - 1) / cs;
-        const int n = (227 * 1024 - kFusedFixed - 128) / fused_stage_bytes<kSaved>(hc, per * 256);
-        if (per <= kFusedMaxWarps && n >= 3) {
-            *stages = std::min(n, 6);
-            return cs;
-        }
-    }
-    return 0;
+// ---- gate with checkpoint, one pass -------------------------------------------------------
+// The same shape for the forward step: phase 1 packs the rows and sums, phase 2
+// turns the gates into hidden + g v from the stage.
+template <bool kF32Kv>
+__host__ __device__ constexpr int ckpt_stage_bytes(int hc, int cols) {
+    return (2 * hc + (hc + 1) * (kF32Kv ? 4 : 2)) * cols;
 }
 
-template <int kSaved, int kHc>
-cudaError_t fused_launch(GateTrain& a, int cs, int stages, int* shares, cudaStream_t s) {
-    auto kern = a.hc == kHc ? k_gate_backward_fused<kSaved, kHc, true> : k_gate_backward_fused<kSaved, kHc, false>;
-    const int per = (a.d / 256 + cs - 1) / cs;
-    const int smem = (kFusedFixed + 127) / 128 * 128 + stages * fused_stage_bytes<kSaved>(a.hc, per * 256);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cs;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    const int clusters = (int)std::min<int64_t>(a.T, device_sm_count() / cs);
-    cfg.gridDim = dim3(clusters * cs);
-    cfg.blockDim = dim3((per + 2) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = cs > 1 ? 2 : 1;
-    *shares = clusters;
-    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs);
+__device__ __forceinline__ uint2 encode_mx8(const f32x2 (&v)[4], uint32_t& exponent) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 x = unpair(v[j]);
+        f[2 * j] = x.x;
+        f[2 * j + 1] = x.y;
+    }
+    return encode_mx8(f, exponent);
+}
+
+template <bool kF32Kv, int kHc, bool kExact>
+__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
+k_gate_checkpoint_fused(const GateTrain a, int stages, int cs) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kSums = 4 * kHc;  // (three used per branch)
+    const int hc = kExact ? kHc : a.hc;
+    const int d = a.d;
+    const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
+    const int groups = d / 256;
+    const int g0 = groups * rank / cs, warps = groups * (rank + 1) / cs - g0;
+    const int max_cols = ((groups + cs - 1) / cs) * 256;
+    const int cols = warps * 256, col0 = g0 * 256;
+    const int stage_bytes = ckpt_stage_bytes<kF32Kv>(hc, max_cols);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int loader = (int)(blockDim.x >> 5) - 2, joiner = loader + 1;
+
+    float* wred = reinterpret_cast<float*>(smem);            // [slots][warps][32]
+    float* red = wred + kFusedSlots * kFusedMaxWarps * 32;   // [slots][8 ranks][32]
+    float* gate = red + kFusedSlots * 8 * 32;                // [slots][8]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(gate + kFusedSlots * 32);
+    volatile int* aborted = reinterpret_cast<volatile int*>(bars + 2 * kFusedMaxStages + 3 * kFusedSlots);
+    uint8_t* ring = smem + (kFusedFixed + 127) / 128 * 128;
+    auto bar = [&](int s) { return smem_u32(bars + s); };
+    auto full = [&](int s) { return bar(s); };
+    auto empty = [&](int s) { return bar(kFusedMaxStages + s); };
+    auto parts = [&](int i) { return bar(2 * kFusedMaxStages + i % kFusedSlots); };
+    auto sums_in = [&](int i) { return bar(2 * kFusedMaxStages + kFusedSlots + i % kFusedSlots); };
+    auto gates_in = [&](int i) { return bar(2 * kFusedMaxStages + 2 * kFusedSlots + i % kFusedSlots); };
+    auto slot_phase = [&](int i) { return (uint32_t)(i / kFusedSlots) & 1u; };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full(s), 1u);
+            mbar_init(empty(s), (uint32_t)warps);
+        }
+        for (int s = 0; s < kFusedSlots; ++s) {
+            mbar_init(parts(s), (uint32_t)warps);
+            mbar_init(sums_in(s), (uint32_t)cs);
+            mbar_init(gates_in(s), 1u);
+        }
+        *aborted = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (cs > 1) cluster_sync();
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int64_t cluster = blockIdx.x / cs, clusters = gridDim.x / cs;
+    const int n = (int)((a.T - cluster + clusters - 1) / clusters);
+    auto token = [&](int i) { return cluster + (int64_t)i * clusters; };
+    auto ready = [&](bool ok) {
+        if (ok) return true;
+        *aborted = 1;
+        atomicOr(a.err, kErrTimeout);
+        return false;
+    };
+    auto wait = [&](uint32_t b, uint32_t phase) {
+        return __all_sync(0xFFFFFFFFu, ready(mbar_wait(b, phase, aborted, a.wait_limit_ns)));
+    };
+
+    if (warp == loader) {
+        for (int i = 0; i < n; ++i) {
+            const int s = i % stages;
+            if (!wait(empty(s), ((uint32_t)(i / stages) & 1u) ^ 1u)) break;
+            const int64_t t = token(i);
+            const uint32_t base = smem_u32(ring + s * stage_bytes);
+            if (lane == 0) mbar_expect_tx(full(s), (uint32_t)ckpt_stage_bytes<kF32Kv>(hc, cols));
+            __syncwarp();
+            for (int r = lane; r < 2 * hc + 1; r += 32) {
+                const int size = r < hc || !kF32Kv ? 2 : 4;
+                const char* src = r < hc ? reinterpret_cast<const char*>(a.hidden + (t * hc + r) * d)
+                                         : static_cast<const char*>(a.kv) + (t * (hc + 1) + (r - hc)) * d * size;
+                const int off = (r < hc ? 2 * r : 2 * hc + size * (r - hc)) * max_cols;
+                bulk_load(base + (uint32_t)off, src + (int64_t)col0 * size, (uint32_t)(cols * size), full(s));
+            }
+        }
+    } else if (warp == joiner) {
+        for (int i = 0; i < n; ++i) {
+            const int slot = i % kFusedSlots;
+            const int64_t t = token(i);
+            const bool image = a.windows[t].x == kDead;  // (on its way during the wait)
+            if (!wait(parts(i), slot_phase(i))) break;
+            float s = 0.f;
+            if (lane < kSums)
+                for (int x = 0; x < warps; ++x) s += wred[(slot * kFusedMaxWarps + x) * 32 + lane];
+            float* out = red + (slot * 8 + rank) * 32 + lane;
+            if (cs == 1) {
+                *out = s;
+                __syncwarp();
+            } else {
+                const uint32_t at = smem_u32(out);
+                for (int r = 0; r < cs; ++r)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_rank(at, (uint32_t)r)), "f"(s)
+                                 : "memory");
+                __syncwarp();
+                if (lane < cs) mbar_arrive_cluster(map_rank(sums_in(i), (uint32_t)lane));
+                if (!__all_sync(0xFFFFFFFFu, ready(mbar_wait_cluster(sums_in(i), slot_phase(i), aborted,
+                                                                     a.wait_limit_ns))))
+                    break;
+            }
+            if (lane < hc) {
+                float x[3] = {};
+                for (int r = 0; r < cs; ++r) {
+                    const float4 y = *reinterpret_cast<const float4*>(red + (slot * 8 + r) * 32 + 4 * lane);
+                    x[0] += y.x; x[1] += y.y; x[2] += y.z;
+                }
+                const float g = image ? 0.f : gate_from_sums(x[0], x[1], x[2], d, a.eps);
+                gate[slot * 8 + lane] = g;
+                if (a.gates && rank == 0) a.gates[t * hc + lane] = g;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(gates_in(i));
+        }
+    } else if (warp < warps) {
+        const int lc = warp * 256 + lane * 8;
+        f32x2 w[kHc][4];
+#pragma unroll
+        for (int b = 0; b < kHc; ++b)
+            if (kExact || b < hc) {
+                float f[8];
+                load8_f32(a.wqk + (int64_t)b * d + col0 + lc, f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[b][j] = pair(f[2 * j], f[2 * j + 1]);
+            }
+        auto hidden_raw = [&](const uint8_t* st, int b) {
+            return *reinterpret_cast<const uint4*>(st + 2 * (b * max_cols + lc));
+        };
+        auto keyvalue = [&](const uint8_t* st, int r, f32x2 (&f)[4]) {
+            if (kF32Kv) {
+                const ulonglong2* p = reinterpret_cast<const ulonglong2*>(st + 2 * hc * max_cols +
+                                                                          4 * (r * max_cols + lc));
+                const ulonglong2 x = p[0], y = p[1];
+                f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+            } else {
+                unpack8(*reinterpret_cast<const uint4*>(st + 2 * ((hc + r) * max_cols + lc)), f);
+            }
+        };
+        uint32_t id = n > 0 ? a.windows[token(0)].x : 0u, id_before = 0u;
+        for (int i = 0; i <= n; ++i) {
+            // slot 0 of the windows of the tokens in phases 1 and 2, the next one's on its way
+            const bool img = id == kDead, image = id_before == kDead;
+            id_before = id;
+            if (i + 1 < n) id = a.windows[token(i + 1)].x;
+            if (i < n) {
+                const int64_t t = token(i);
+                const int s = i % stages;
+                const uint8_t* st = ring + s * stage_bytes;
+                uint8_t* codes = a.codes_out + t * (int64_t)(2 * hc + 1) * d + col0 + lc;
+                uint8_t* scales = a.scales_out + t * (int64_t)((2 * hc + 1) * (d / 32)) + (col0 + lc) / 32;
+                auto keep = [&](int r, const f32x2 (&f)[4]) {
+                    uint32_t e;
+                    uint2 c = encode_mx8(f, e);
+                    if (img) c = make_uint2(0u, 0u), e = 0u;  // an image row's checkpoint is zero
+                    __stcs(reinterpret_cast<uint2*>(codes + (int64_t)r * d), c);
+                    if ((lane & 3) == 0) scales[r * (d / 32)] = (uint8_t)e;
+                };
+                if (!wait(full(s), (uint32_t)(i / stages) & 1u)) break;
+                float sum[kSums];
+#pragma unroll
+                for (int b = 0; b < kHc; ++b) {
+                    float* sb = sum + 4 * b;
+                    sb[0] = sb[1] = sb[2] = sb[3] = 0.f;
+                    if (!kExact && b >= hc) continue;
+                    f32x2 h[4], k[4];
+                    unpack8(hidden_raw(st, b), h);
+                    keyvalue(st, b, k);
+                    f32x2 q[3] = {0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        q[0] = fma2(k[j], k[j], q[0]);
+                        q[1] = fma2(h[j], h[j], q[1]);
+                        q[2] = fma2(mul2(h[j], w[b][j]), k[j], q[2]);
+                    }
+                    sb[0] = both(q[0]);
+                    sb[1] = both(q[1]);
+                    sb[2] = both(q[2]);
+                    keep(b, h);
+                    keep(hc + b, k);
+                }
+                const float mine = warp_sums<kSums>(sum, lane);
+                constexpr int kPer = 32 / kSums;
+                if (lane % kPer == 0)
+                    wred[((i % kFusedSlots) * kFusedMaxWarps + warp) * 32 + lane / kPer] = mine;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(parts(i));
+                f32x2 v[4];
+                keyvalue(st, hc, v);
+                keep(2 * hc, v);
+            }
+            if (i == 0) continue;
+            const int p = i - 1, s = p % stages;
+            const uint8_t* st = ring + s * stage_bytes;
+            uint16_t* ho = a.hidden_out + token(p) * (int64_t)hc * d + col0 + lc;
+            if (!wait(gates_in(p), slot_phase(p))) break;
+            const float* gp = gate + (p % kFusedSlots) * 8;
+            f32x2 v[4];
+            keyvalue(st, hc, v);
+#pragma unroll
+            for (int b = 0; b < kHc; ++b) {
+                if (!kExact && b >= hc) continue;
+                uint4 o = hidden_raw(st, b);
+                if (!image) {
+                    f32x2 h[4];
+                    unpack8(o, h);
+                    const f32x2 g = pair(gp[b], gp[b]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = fma2(g, v[j], h[j]);
+                    o = pack8(h);
+                }
+                __stcs(reinterpret_cast<uint4*>(ho + (int64_t)b * d), o);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(s));
+        }
+    }
+    __syncthreads();
+    if (*aborted) {  // let copies in flight land
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+        __syncthreads();
+    }
+    if (cs > 1) cluster_sync();  // no arrival may target a CTA that exited
 }
 
 // ---- two passes: geometries whose tokens do not fit ------------------------------------------
@@ -1442,11 +1646,80 @@ k_gate_backward_weights(const GateTrain a, int shares) {
     put(a.dwk, a.wq);
 }
 
+// Cluster size and stages of a one-pass kernel for d columns and a stage of
+// bytes(cols) bytes; 0 if no cluster holds three stages of a token (one in each
+// phase and one on its way).
+template <class Bytes>
+int one_pass_cluster(int d, Bytes bytes, int* stages) {
+    const int groups = d / 256;
+    for (int cs = 1; cs <= 8 && cs <= groups; cs *= 2) {
+        const int per = (groups + cs - 1) / cs;
+        const int n = (227 * 1024 - kFusedFixed - 128) / bytes(per * 256);
+        if (per <= kFusedMaxWarps && n >= 3) {
+            *stages = std::min(n, 6);
+            return cs;
+        }
+    }
+    return 0;
+}
+
+template <class F>
+cudaError_t one_pass_launch(F kern, const GateTrain& a, int cs, int stages, int stage_bytes, int* clusters,
+                            cudaStream_t s) {
+    const int per = (a.d / 256 + cs - 1) / cs;
+    const int smem = (kFusedFixed + 127) / 128 * 128 + stages * stage_bytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    *clusters = (int)std::min<int64_t>(a.T, device_sm_count() / cs);
+    cfg.gridDim = dim3(*clusters * cs);
+    cfg.blockDim = dim3((per + 2) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cs > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs);
+}
+
+template <int kSaved, int kHc>
+cudaError_t fused_launch(const GateTrain& a, int cs, int stages, int* shares, cudaStream_t s) {
+    const int bytes = fused_stage_bytes<kSaved>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
+    return a.hc == kHc ? one_pass_launch(k_gate_backward_fused<kSaved, kHc, true>, a, cs, stages, bytes, shares, s)
+                       : one_pass_launch(k_gate_backward_fused<kSaved, kHc, false>, a, cs, stages, bytes, shares, s);
+}
+
+template <bool kF32Kv, int kHc>
+cudaError_t ckpt_launch(const GateTrain& a, int cs, int stages, cudaStream_t s) {
+    const int bytes = ckpt_stage_bytes<kF32Kv>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
+    int clusters;
+    return a.hc == kHc
+               ? one_pass_launch(k_gate_checkpoint_fused<kF32Kv, kHc, true>, a, cs, stages, bytes, &clusters, s)
+               : one_pass_launch(k_gate_checkpoint_fused<kF32Kv, kHc, false>, a, cs, stages, bytes, &clusters, s);
+}
+
+template <bool kF32Kv>
+cudaError_t gate_checkpoint(const GateTrain& a, cudaStream_t s) {
+    int stages = 0;
+    if (const int cs = one_pass_cluster(a.d, [&](int c) { return ckpt_stage_bytes<kF32Kv>(a.hc, c); }, &stages))
+        return a.hc == 1   ? ckpt_launch<kF32Kv, 1>(a, cs, stages, s)
+               : a.hc == 2 ? ckpt_launch<kF32Kv, 2>(a, cs, stages, s)
+               : a.hc <= 4 ? ckpt_launch<kF32Kv, 4>(a, cs, stages, s)
+                           : ckpt_launch<kF32Kv, 8>(a, cs, stages, s);
+    return pdl_launch(k_gate_checkpoint<kF32Kv>, dim3((unsigned)a.T), dim3(std::min(320, a.d / 8)), 0, s, a);
+}
+
 template <int kSaved>
 cudaError_t gate_backward(GateTrain a, cudaStream_t s) {
     const dim3 wgrid((unsigned)((int64_t)a.hc * a.d / 128));
     int stages = 0, shares = 0;
-    if (const int cs = fused_cluster<kSaved>(a.hc, a.d, &stages)) {
+    if (const int cs = one_pass_cluster(a.d, [&](int c) { return fused_stage_bytes<kSaved>(a.hc, c); }, &stages)) {
         cudaError_t e = a.hc == 1   ? fused_launch<kSaved, 1>(a, cs, stages, &shares, s)
                         : a.hc == 2 ? fused_launch<kSaved, 2>(a, cs, stages, &shares, s)
                         : a.hc <= 4 ? fused_launch<kSaved, 4>(a, cs, stages, &shares, s)
@@ -1562,8 +1835,7 @@ cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
 }
 
 cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t s) {
-    return pdl_launch(kv_f32 ? k_gate_checkpoint<true> : k_gate_checkpoint<false>,
-                      dim3((unsigned)a.T), dim3(std::min(320, a.d / 8)), 0, s, a);
+    return kv_f32 ? gate_checkpoint<true>(a, s) : gate_checkpoint<false>(a, s);
 }
 
 int gate_backward_shares(int64_t T, int d) {

@@ -288,6 +288,12 @@ def test_gate_checkpoint(T, hc, d, kv_format):
     s.close()
 
 
+@pytest.mark.parametrize("kv_format", [eg.KV_F32, eg.KV_BF16])
+@pytest.mark.parametrize("T,hc,d", [(700, 2, 256), (320, 4, 5120), (3, 8, 9216), (2, 1, 20_736)])
+def test_gate_checkpoint_of_many_and_of_wide_tokens(T, hc, d, kv_format):
+    test_gate_checkpoint(T, hc, d, kv_format)
+
+
 def test_gate_checkpoint_of_infinities_and_nans():
     T, hc, d = 1, 1, 256
     h, kv, win, wq, wk = gate_problem(T, hc, d, 5, image=())
