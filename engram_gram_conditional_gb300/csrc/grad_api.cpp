@@ -52,7 +52,8 @@ engram_status check_embed(uint64_t rows, uint32_t dim, int64_t n, uint32_t copie
 }
 
 struct EmbedWs {
-    uint32_t *keys0, *keys1, *vals0, *vals1, *hist, *digit_total, *block_heads, *barrier, *n_valid,
+    uint2 *pairs0, *pairs1;
+    uint32_t *hist, *digit_total, *block_heads, *barrier, *n_valid,
         *segpos, *seg_start, *unique, *count;
     float* partial;
     size_t bytes;
@@ -64,10 +65,8 @@ EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
     const size_t blocks = embed_sort_blocks(n), bins = (size_t)1 << bits;
     Carver c(p);
     EmbedWs w{};
-    w.keys0 = c.take<uint32_t>(n);
-    w.keys1 = c.take<uint32_t>(n);
-    w.vals0 = c.take<uint32_t>(n);
-    w.vals1 = c.take<uint32_t>(n);
+    w.pairs0 = c.take<uint2>(n);
+    w.pairs1 = c.take<uint2>(n);
     w.hist = c.take<uint32_t>(blocks * bins);
     w.digit_total = c.take<uint32_t>(bins);
     w.block_heads = c.take<uint32_t>(blocks);
@@ -276,10 +275,8 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
     a.n = n;
     a.rows = rows;
     embed_sort_digits(rows, &a.passes, &a.digit_bits);
-    a.keys0 = w.keys0;
-    a.keys1 = w.keys1;
-    a.vals0 = w.vals0;
-    a.vals1 = w.vals1;
+    a.pairs0 = w.pairs0;
+    a.pairs1 = w.pairs1;
     a.hist = w.hist;
     a.digit_total = w.digit_total;
     a.block_heads = w.block_heads;
@@ -294,7 +291,7 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
     e = launch_embed_sort(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "embed sort launch");
     EmbedSum u{};
-    u.perm = a.passes & 1 ? w.vals1 : w.vals0;
+    u.sorted = a.passes & 1 ? w.pairs1 : w.pairs0;
     u.segpos = w.segpos;
     u.seg_start = w.seg_start;
     u.unique = a.unique;

@@ -69,7 +69,7 @@ struct EmbedSort {
     int64_t n;
     uint64_t rows;           // ids at or above are not rows
     int passes, digit_bits;  // embed_sort_digits
-    uint32_t *keys0, *keys1, *vals0, *vals1;  // [n]; the sorted pair is number passes & 1
+    uint2 *pairs0, *pairs1;  // (id, position) [n]; the sorted one is number passes & 1
     uint32_t* hist;          // [2^digit_bits][blocks]
     uint32_t* digit_total;   // [2^digit_bits]
     uint32_t* block_heads;   // [blocks]
@@ -87,7 +87,8 @@ void embed_sort_digits(uint64_t rows, int* passes, int* bits);
 cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s);
 // The rows' sums: grad[segment or, dense, its id] = scale x the sum of its rows of dout.
 struct EmbedSum {
-    const uint32_t *perm, *segpos, *seg_start, *unique, *n_valid;
+    const uint2* sorted;     // (id, position)
+    const uint32_t *segpos, *seg_start, *unique, *n_valid;
     const uint16_t* dout;    // bf16 [n][copies][dim]
     int dim, copies;
     float scale;

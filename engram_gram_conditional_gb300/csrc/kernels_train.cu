@@ -87,28 +87,30 @@ constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kSortBatch = 8;  // rounds of 32 keys that a warp loads at once
 constexpr int kSmallSort = kSortThreads * 8;  // keys of the one-cluster sort
 
-// A barrier of the cooperative launch's blocks, bounded: false on a time-out.
-__device__ __forceinline__ bool grid_barrier(const EmbedSort& a, uint32_t& phase, int* flag) {
+// A barrier of the cooperative launch's blocks in two halves, so that a block can
+// work between them; the wait is bounded: false on a time-out.
+__device__ __forceinline__ void grid_arrive(const EmbedSort& a) {
     __syncthreads();
-    if (gridDim.x > 1) {
-        if (threadIdx.x == 0) {
-            ++phase;
-            const uint32_t want = phase * gridDim.x;
-            __threadfence();
-            atomicAdd(a.barrier, 1u);
-            const uint64_t t0 = globaltimer();
-            uint32_t spin = 0;
-            while (ld_acquire_u32(a.barrier) < want) {
-                if ((++spin & 63u) == 0u && (long long)(globaltimer() - t0) > a.wait_limit_ns) {
-                    atomicOr(a.err, kErrTimeout);
-                    *flag = 1;
-                    break;
-                }
-            }
-            __threadfence();
-        }
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        atomicAdd(a.barrier, 1u);
     }
+}
+__device__ __forceinline__ bool grid_wait(const EmbedSort& a, uint32_t& phase, int* flag) {
+    if (threadIdx.x == 0) {
+        const uint32_t want = ++phase * gridDim.x;
+        const uint64_t t0 = globaltimer();
+        uint32_t spin = 0;
+        while (ld_acquire_u32(a.barrier) < want) {
+            if ((++spin & 63u) == 0u && (long long)(globaltimer() - t0) > a.wait_limit_ns) {
+                atomicOr(a.err, kErrTimeout);
+                *flag = 1;
+                break;
+            }
+        }
+        __threadfence();
+    }
+    __syncthreads();
     return *flag == 0;
 }
 
@@ -212,18 +214,19 @@ __device__ __forceinline__ void put_segments(const EmbedSort& a, const Heads& h,
 }
 
 // Stable radix sort of (id, position), least significant digit first, then the
-// segments of equal ids.  A block owns a contiguous range of the keys and a
-// warp a contiguous part of it, so the order of equal digits is kept: per pass,
-// every warp counts its digits (one of the lanes with equal digits adds their
-// number), the counts are turned into first places over (digit, block, warp),
-// and each warp hands them out in key order.  Ids that are masked or outside
-// the table become `rows`, the largest key: they sort behind every row and take
-// no part.  kOne: a warp's keys are one batch, which stays in registers with the
-// places found while counting.
-template <bool kOne>
+// segments of equal ids.  A block owns a contiguous range of the keys, in tiles
+// of up to 8,192, a warp a contiguous part of a tile, so the order of equal
+// digits is kept.  Per pass: every warp counts its digits (one of the lanes with
+// equal digits adds their number); the counts become first places over (digit,
+// block); the tile is put in digit order in shared memory and leaves in runs of
+// equal digits.  (Written from where they lay, each key to a sector of its own,
+// 1.2 million keys took 30 us a pass, bound by L2's sectors.)  Ids that are
+// masked or outside the table become `rows`, the largest key: they sort behind
+// every row and take no part.
 __global__ void __launch_bounds__(kSortThreads)
 k_embed_sort(const EmbedSort a) {
-    extern __shared__ uint32_t cnt[];  // [kSortWarps][bins]
+    extern __shared__ uint32_t cnt[];  // [kSortWarps][bins], then the tile in digit order
+    __shared__ uint32_t place[512];    // of the block's next key of each digit, less its place in the tile
     __shared__ uint32_t warp_sum[kSortWarps];
     __shared__ uint32_t shared_base;
     __shared__ int flag;
@@ -232,66 +235,92 @@ k_embed_sort(const EmbedSort a) {
     const int B = (int)gridDim.x, b = (int)blockIdx.x;
     const int bins = 1 << a.digit_bits;
     const uint32_t dmask = (uint32_t)bins - 1u;
-    // ranges in whole rounds of 32 keys
+    uint2* const tile = reinterpret_cast<uint2*>(cnt + kSortWarps * bins);
+    // ranges in whole multiples of 32 keys; a tile is `per` keys of every warp
     const int64_t rounds = (a.n + 31) / 32;
-    const int64_t r0 = rounds * b / B, r1 = rounds * (b + 1) / B;
-    const int64_t w0 = r0 + (r1 - r0) * warp / kSortWarps;
-    const int64_t w1 = r0 + (r1 - r0) * (warp + 1) / kSortWarps;
+    const int64_t lo = rounds * b / B * 32, hi = min(rounds * (b + 1) / B * 32, a.n);
+    const int per = (int)min((int64_t)kSortBatch, (hi - lo + kSortThreads - 1) / kSortThreads);  // rounds
+    const int64_t tile_keys = (int64_t)per * kSortThreads;
+    const bool one = hi - lo <= tile_keys;
     uint32_t phase = 0;
     if (threadIdx.x == 0) flag = 0;
     __syncthreads();
     const uint32_t rows = (uint32_t)a.rows;
     uint32_t* const mine = cnt + warp * bins;
+    const bool has_digit = (int)threadIdx.x < bins;  // (bins <= 512)
 
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * a.digit_bits;
-        const uint32_t* kin = pass & 1 ? a.keys1 : a.keys0;
-        const uint32_t* vin = pass & 1 ? a.vals1 : a.vals0;
-        uint32_t* kout = pass & 1 ? a.keys0 : a.keys1;
-        uint32_t* vout = pass & 1 ? a.vals0 : a.vals1;
-        uint32_t k[kSortBatch], v[kSortBatch], at[kSortBatch];
-        auto load = [&](int64_t r) {
+        const uint2* in = pass & 1 ? a.pairs1 : a.pairs0;
+        uint2* out = pass & 1 ? a.pairs0 : a.pairs1;
+        uint2 kv[kSortBatch];
+        uint32_t at[kSortBatch];
+        auto key_index = [&](int64_t t0, int u) { return t0 + (warp * per + u) * 32 + lane; };
+        auto load = [&](int64_t t0) {
 #pragma unroll
             for (int u = 0; u < kSortBatch; ++u) {
-                const int64_t i = (r + u) * 32 + lane;
-                k[u] = v[u] = 0u;
-                if (r + u < w1 && i < a.n) {
-                    k[u] = pass ? __ldcg(kin + i) : min(a.ids[i], rows);
-                    v[u] = pass ? __ldcg(vin + i) : (uint32_t)i;
-                }
+                if (u >= per) break;
+                const int64_t i = key_index(t0, u);
+                kv[u] = make_uint2(0u, 0u);
+                if (i < hi) kv[u] = pass ? __ldcg(in + i) : make_uint2(min(a.ids[i], rows), (uint32_t)i);
             }
         };
-        auto rank = [&](int64_t r) {
+        // a key's place among its warp's keys of the same digit
+        auto rank = [&](int64_t t0) {
+            for (int i = lane; i < bins; i += 32) mine[i] = 0;
+            __syncwarp();
 #pragma unroll
             for (int u = 0; u < kSortBatch; ++u) {
-                const bool on = r + u < w1 && (r + u) * 32 + lane < a.n;
+                if (u >= per) break;
+                const bool on = key_index(t0, u) < hi;
                 const uint32_t all_on = __ballot_sync(0xFFFFFFFFu, on);
-                const uint32_t d = (k[u] >> shift) & dmask;
+                const uint32_t d = (kv[u].x >> shift) & dmask;
                 const uint32_t same = same_digit(d, a.digit_bits, all_on);
                 at[u] = on ? mine[d] + __popc(same & lt) : 0u;
                 __syncwarp();
                 if (on && (same & lt) == 0u) mine[d] += __popc(same);
                 __syncwarp();
             }
+            __syncthreads();
         };
-        for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
-        __syncthreads();
-        for (int64_t r = w0; r < w1; r += kSortBatch) {
-            load(r);
-            if (pass == 0) {
+        // the tile in digit order; `total`: the tile's keys of this thread's digit
+        auto reorder = [&](int64_t t0, uint32_t total) {
+            uint32_t all;
+            const uint32_t start = block_scan(total, warp_sum, &all);
+            add_warps(cnt, bins, start);
+            __syncthreads();
 #pragma unroll
-                for (int u = 0; u < kSortBatch; ++u) {
-                    const int64_t i = (r + u) * 32 + lane;
-                    if (r + u < w1 && i < a.n && k[u] == rows && a.ids[i] != kMasked)
-                        atomicOr(a.err, kErrBounds);
-                }
+            for (int u = 0; u < kSortBatch; ++u) {
+                if (u >= per) break;
+                if (key_index(t0, u) < hi) tile[at[u] + mine[(kv[u].x >> shift) & dmask]] = kv[u];
             }
-            rank(r);
+            __syncthreads();
+            return start;
+        };
+        uint32_t total = 0, start = 0;
+        if (one) {
+            load(lo);
+            rank(lo);
+            total = scan_warps(cnt, bins);
+        } else {  // only the counts of the whole range
+            for (int i = threadIdx.x; i < bins; i += kSortThreads) cnt[i] = 0;
+            __syncthreads();
+            for (int64_t t0 = lo; t0 < hi; t0 += tile_keys) {
+                load(t0);
+#pragma unroll
+                for (int u = 0; u < kSortBatch; ++u)
+                    if (key_index(t0, u) < hi) atomicAdd(cnt + ((kv[u].x >> shift) & dmask), 1u);
+            }
+            __syncthreads();
+            total = has_digit ? cnt[threadIdx.x] : 0u;
         }
-        __syncthreads();
-        const uint32_t total = scan_warps(cnt, bins);
-        if ((int)threadIdx.x < bins) __stcg(a.hist + (int64_t)threadIdx.x * B + b, total);
-        if (!grid_barrier(a, phase, &flag)) return;
+        if (pass == 0)  // ids outside the table
+            for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
+                if (a.ids[i] >= rows && a.ids[i] != kMasked) atomicOr(a.err, kErrBounds);
+        if (has_digit) __stcg(a.hist + (int64_t)threadIdx.x * B + b, total);
+        grid_arrive(a);
+        if (one) start = reorder(lo, total);
+        if (!grid_wait(a, phase, &flag)) return;
         // first place of each (digit, block) within its digit
         for (int d = b * kSortWarps + warp; d < bins; d += B * kSortWarps) {
             uint32_t run = 0;
@@ -309,38 +338,40 @@ k_embed_sort(const EmbedSort a) {
             }
             if (lane == 0) __stcg(a.digit_total + d, run);
         }
-        if (!grid_barrier(a, phase, &flag)) return;
-        const int d = (int)threadIdx.x;
+        grid_arrive(a);
+        if (!grid_wait(a, phase, &flag)) return;
         uint32_t all;
-        const uint32_t base = block_scan(d < bins ? __ldcg(a.digit_total + d) : 0u, warp_sum, &all);
-        add_warps(cnt, bins, d < bins ? base + __ldcg(a.hist + (int64_t)d * B + b) : 0u);
-        __syncthreads();
-        for (int64_t r = w0; r < w1; r += kSortBatch) {
-            if (!kOne) {
-                load(r);
-                rank(r);
+        const uint32_t base = block_scan(has_digit ? __ldcg(a.digit_total + threadIdx.x) : 0u, warp_sum, &all);
+        uint32_t next = has_digit ? base + __ldcg(a.hist + (int64_t)threadIdx.x * B + b) : 0u;
+        for (int64_t t0 = lo; t0 < hi; t0 += tile_keys) {
+            if (!one) {
+                load(t0);
+                rank(t0);
+                total = scan_warps(cnt, bins);
+                start = reorder(t0, total);
             }
-#pragma unroll
-            for (int u = 0; u < kSortBatch; ++u) {
-                if (r + u < w1 && (r + u) * 32 + lane < a.n) {
-                    const uint32_t p = at[u] + (kOne ? mine[(k[u] >> shift) & dmask] : 0u);
-                    __stcg(kout + p, k[u]);
-                    __stcg(vout + p, v[u]);
-                }
+            if (has_digit) place[threadIdx.x] = next - start;
+            next += total;
+            __syncthreads();
+            const int count = (int)min(tile_keys, hi - t0);
+            for (int i = threadIdx.x; i < count; i += kSortThreads) {
+                const uint2 x = tile[i];
+                __stcg(out + (place[(x.x >> shift) & dmask] + (uint32_t)i), x);
             }
+            __syncthreads();
         }
-        if (!grid_barrier(a, phase, &flag)) return;
+        grid_arrive(a);
+        if (!grid_wait(a, phase, &flag)) return;
     }
 
     // segments of equal ids among the ids of table rows
-    const uint32_t* keys = a.passes & 1 ? a.keys1 : a.keys0;
-    const int64_t lo = r0 * 32, hi = min(r1 * 32, a.n);
+    const uint2* pairs = a.passes & 1 ? a.pairs1 : a.pairs0;
     auto heads_at = [&](int64_t i0) {
         uint32_t key[kSortBatch];
 #pragma unroll
-        for (int u = 0; u < kSortBatch; ++u) key[u] = i0 + u < hi ? __ldcg(keys + i0 + u) : rows;
-        const uint32_t before = i0 > 0 && i0 < hi ? __ldcg(keys + i0 - 1) : rows;
-        const uint32_t after = i0 + kSortBatch < a.n ? __ldcg(keys + i0 + kSortBatch) : rows;
+        for (int u = 0; u < kSortBatch; ++u) key[u] = i0 + u < hi ? __ldcg(pairs + i0 + u).x : rows;
+        const uint32_t before = i0 > 0 && i0 < hi ? __ldcg(pairs + i0 - 1).x : rows;
+        const uint32_t after = i0 + kSortBatch < a.n ? __ldcg(pairs + i0 + kSortBatch).x : rows;
         // (hi is a multiple of eight unless it is n: `after` is the next place's key)
         return find_heads(key, before, after, i0, hi < a.n && i0 + kSortBatch >= hi ? hi + 1 : hi, rows);
     };
@@ -350,11 +381,12 @@ k_embed_sort(const EmbedSort a) {
         heads += __popc(h.begins);
         if (h.last) __stcg(a.n_valid, (uint32_t)(i0 + __ffs(h.last)));
     }
-    if (b == 0 && threadIdx.x == 0 && __ldcg(keys) >= rows) __stcg(a.n_valid, 0u);
+    if (b == 0 && threadIdx.x == 0 && __ldcg(pairs).x >= rows) __stcg(a.n_valid, 0u);
     uint32_t block_heads;
     block_scan(heads, warp_sum, &block_heads);
     if (threadIdx.x == 0) __stcg(a.block_heads + b, block_heads);
-    if (!grid_barrier(a, phase, &flag)) return;
+    grid_arrive(a);
+    if (!grid_wait(a, phase, &flag)) return;
     if (warp == 0) {
         uint32_t before = 0, all = 0;
         for (int x = lane; x < B; x += 32) {
@@ -452,7 +484,7 @@ k_embed_sort_small(const EmbedSort a) {
         v = vals[to][threadIdx.x];
     }
     // the sorted positions and the segments
-    if (i < n) (a.passes & 1 ? a.vals1 : a.vals0)[i] = v;
+    if (i < n) (a.passes & 1 ? a.pairs1 : a.pairs0)[i] = make_uint2(k, v);
     const int in = (a.passes - 1) & 1;
     if (threadIdx.x == 0) edge[0] = k;
     if (threadIdx.x == kSortThreads - 1) edge[1] = k;
@@ -555,7 +587,7 @@ k_embed_sum(const EmbedSum a) {
         seg = row = 0u;
         if (i + l < count) {
             seg = a.segpos[lo + i + l];
-            row = a.perm[lo + i + l];
+            row = a.sorted[lo + i + l].y;
         }
     };
     uint32_t seg, row;
@@ -1760,8 +1792,9 @@ cudaError_t launch_embed(const void* table, bool f32, uint64_t rows, int dim, co
                       dim3(256), 0, s, table, rows, dim, ids, n, scale, copies, lanes, out, err);
 }
 
+// A block per 1,024 keys, a key per thread, until every SM has one.
 int embed_sort_blocks(int64_t n) {
-    return (int)std::min<int64_t>(device_sm_count(), std::max<int64_t>(1, (n + 8191) / 8192));
+    return (int)std::min<int64_t>(device_sm_count(), std::max<int64_t>(1, (n + kSortThreads - 1) / kSortThreads));
 }
 
 void embed_sort_digits(uint64_t rows, int* passes, int* bits) {
@@ -1796,16 +1829,13 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
         return cudaLaunchKernelEx(&cfg, k_embed_sort_small, a);
     }
     const int blocks = embed_sort_blocks(a.n);
-    const int smem = kSortWarps * (1 << a.digit_bits) * 4;
-    // a warp's rounds of 32 keys, at most
-    const int64_t per_warp = (((a.n + 31) / 32 + blocks - 1) / blocks + kSortWarps - 1) / kSortWarps;
-    auto f = per_warp <= kSortBatch ? k_embed_sort<true> : k_embed_sort<false>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = kSortWarps * (1 << a.digit_bits) * 4 + kSortThreads * kSortBatch * 8;
+    cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = cudaMemsetAsync(a.barrier, 0, 4, s);
     if (e != cudaSuccess) return e;
     EmbedSort copy = a;
     void* args[] = {&copy};
-    return cudaLaunchCooperativeKernel((void*)f, dim3(blocks), dim3(kSortThreads), args, smem, s);
+    return cudaLaunchCooperativeKernel((void*)k_embed_sort, dim3(blocks), dim3(kSortThreads), args, smem, s);
 }
 
 // Sorted places per chunk: 64 rows of dout (a chunk's two partial rows are then
