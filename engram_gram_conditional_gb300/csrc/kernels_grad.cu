@@ -87,17 +87,25 @@ __device__ __forceinline__ uint32_t out_piece(uint32_t box, int r, int j) {
 // are written.
 __device__ __forceinline__ void put_box(uint32_t box, int lane, uint16_t* dst, int64_t ld, int64_t rows,
                                         int64_t cols) {
-    const int j = lane & 7;
+    const int j = lane & 7, r0 = lane >> 3;
+    const int n = 8 * j < cols ? (int)min(rows, (int64_t)32) : 0;
+    dst += r0 * ld + 8 * j;
+    uint4 v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int r = 4 * k + (lane >> 3);
-        uint4 v;
+    for (int k = 0; k < 8; ++k)
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(out_piece(box, r, j))
-                     : "memory");
-        if (r < rows && 8 * j < cols) *reinterpret_cast<uint4*>(dst + r * ld + 8 * j) = v;
-    }
+                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                     : "r"(out_piece(box, 4 * k + r0, j)));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (4 * k + r0 < n) *reinterpret_cast<uint4*>(dst + 4 * k * ld) = v[k];
+}
+// Arrival on a barrier of the pair's even CTA that hands an accumulator back.  A
+// release at CTA scope: what it orders is this warp's reads of tensor memory,
+// which tcgen05.wait::ld has completed.  At cluster scope it would wait for the
+// warp's stores of the tile before (850 to 2,200 cycles per tile).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // 32 bytes at a time: a whole sector per thread.
 __device__ __forceinline__ void ld_global_v8(const float* p, float (&f)[8]) {
@@ -340,7 +348,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
         auto acc_done = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(tempty(use & 1), 0));
+            if (lane == 0) mbar_arrive_remote(map_rank(tempty(use & 1), 0));
             ++use;
         };
         for (int i = 0; i < n_items; ++i) {
@@ -458,9 +466,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                 }
             } else if constexpr (kEpi == kGradOut) {
                 if (!q.acc) {
-                    // the accumulator is handed back before the first store: the
-                    // arrival is a release, which waits for the stores before it
-                    // (1,200 to 2,600 cycles)
+                    // the accumulator is handed back before the first store
                     uint32_t o[4][16];
 #pragma unroll
                     for (int c = 0; c < 4; c += 2) {
@@ -627,10 +633,10 @@ void share_items(GradArgs& a, int pairs) {
     a.rounds_fewer = 0;
     if (!a.pr[0].items || !a.pr[1].items || !a.pairs_more) return;
     // an item takes its k-blocks and a little; a short one what writing out its
-    // tile takes (measured: 11 k-blocks' time at one k-block, 14 at six, 34 at 32)
+    // tile takes (measured: 7 k-blocks' time at one k-block, 11 at six, 34 at 32)
     auto cost = [](const GradProblem& q) {
         const double kb = (double)q.kb / q.splits;
-        return std::max(kb + 2.0, 11.0 + 0.5 * kb);
+        return std::max(kb + 2.0, 7.0 + 0.7 * kb);
     };
     const int fewer = pairs - a.pairs_more;
     a.rounds_fewer = std::min((int)(cost(a.pr[0]) / cost(a.pr[1]) + 0.5), (a.pr[1].items + fewer - 1) / fewer);
