@@ -175,6 +175,11 @@ engram_status check_loss(uint32_t vocab, uint32_t dim, int64_t T) {
     return check_T(T);
 }
 
+// Column groups whose (maximum, sum) pairs a row's loss is joined from.
+int loss_groups(int64_t T, uint32_t vocab) {
+    return T <= kFewTokens ? few_groups(vocab) : (int)ceil_div(vocab, kBN) * 2;
+}
+
 int loss_group_m(uint32_t dim) {  // M units whose x rows (40 MB) stay in L2 beside the head
     return (int)std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)40 << 20) / (512 * (int64_t)dim)));
 }
@@ -189,6 +194,16 @@ int64_t loss_piece(int64_t T, uint32_t vocab) {
     int64_t tiles = std::max<int64_t>(16, waves >= 1 ? waves * P / units : P / units);
     tiles = std::min(std::max<int64_t>(1, tiles), all);
     return tiles * kBN;
+}
+
+FewArgs few_args(const engram_ctx* ctx, int64_t T, uint32_t vocab, uint32_t dim) {
+    FewArgs f{};
+    f.T = (int)T;
+    f.kb = (int)ceil_div(dim, kBK);
+    f.vocab = (int)vocab;
+    f.err = ctx->d_err;
+    f.wait_limit_ns = ctx->wait_limit_ns;
+    return f;
 }
 
 struct LossBackWs {
@@ -459,7 +474,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
 size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
     if (check_loss(vocab, dim, T)) return 0;
     Carver c(nullptr);
-    c.take<float2>((size_t)ceil_div(vocab, kBN) * 2 * T);
+    c.take<float2>((size_t)loss_groups(T, vocab) * T);
     c.take<float>(T);
     return c.bytes();
 }
@@ -477,28 +492,37 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
     if ((st = train_device(ctx))) return st;
     const cudaStream_t s = (cudaStream_t)stream;
     Carver c(d_workspace);
-    const int n_tiles = (int)ceil_div(vocab, kBN);
-    float2* part = c.take<float2>((size_t)n_tiles * 2 * T);
+    const int groups = loss_groups(T, vocab);
+    float2* part = c.take<float2>((size_t)groups * T);
     float* zlabel = c.take<float>(T);
-    GradArgs a{};
-    a.err = ctx->d_err;
-    a.wait_limit_ns = ctx->wait_limit_ns;
-    a.pr[0] = product(T, n_tiles * (int64_t)kBN, dim, false);
-    a.pr[0].group_m = loss_group_m(dim);
-    a.T = T;
-    a.vocab = (int)vocab;
-    a.labels = d_labels;
-    a.zlabel = zlabel;
-    a.part = part;
-    CUtensorMap tm[4];
-    cudaError_t e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
-    if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
-    if (e != cudaSuccess) return cuda_fail(e, "loss tensor maps");
-    tm[2] = tm[0], tm[3] = tm[1];
-    e = launch_grad_lse(a, tm, s);
+    cudaError_t e;
+    if (T <= kFewTokens) {
+        FewArgs f = few_args(ctx, T, vocab, dim);
+        f.rows = (int)vocab;
+        f.labels = d_labels;
+        f.zlabel = zlabel;
+        f.part = part;
+        e = launch_few_lse(f, d_x, d_head, (int)dim, s);
+    } else {
+        GradArgs a{};
+        a.err = ctx->d_err;
+        a.wait_limit_ns = ctx->wait_limit_ns;
+        a.pr[0] = product(T, vocab, dim, false);
+        a.pr[0].group_m = loss_group_m(dim);
+        a.T = T;
+        a.vocab = (int)vocab;
+        a.labels = d_labels;
+        a.zlabel = zlabel;
+        a.part = part;
+        CUtensorMap tm[4];
+        e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
+        if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
+        if (e != cudaSuccess) return cuda_fail(e, "loss tensor maps");
+        tm[2] = tm[0], tm[3] = tm[1];
+        e = launch_grad_lse(a, tm, s);
+    }
     if (e == cudaSuccess)
-        e = launch_loss_combine(part, n_tiles * 2, T, zlabel, d_labels, (int)vocab, d_loss, d_lse,
-                                ctx->d_err, s);
+        e = launch_loss_combine(part, groups, T, zlabel, d_labels, (int)vocab, d_loss, d_lse, ctx->d_err, s);
     if (e != cudaSuccess) return cuda_fail(e, "loss launch");
     return ok();
 }
@@ -538,25 +562,37 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         const bool first = v0 == 0, last = v0 + step >= vocab;
         const uint16_t* head = d_head + v0 * dim;
         // z of the piece, and dz from it
-        GradArgs a{};
-        a.err = ctx->d_err;
-        a.wait_limit_ns = ctx->wait_limit_ns;
-        a.pr[0] = product(T, piece, dim, false);
-        a.pr[0].group_m = loss_group_m(dim);
-        a.T = T;
-        a.v0 = v0;
-        a.vocab = (int)vocab;
-        a.dz_chunks = (int)(piece / 64);
-        a.labels = d_labels;
-        a.lse = d_lse;
-        a.dloss = d_dloss;
-        a.dz = w.dz;
         CUtensorMap tm[4];
-        tm[0] = tm[2] = x_k;
-        e = make_tma_16bit(&tm[1], head, vocab - v0, dim, kBM, false);
+        if (T <= kFewTokens) {
+            FewArgs f = few_args(ctx, T, vocab, dim);
+            f.rows = (int)piece;
+            f.v0 = v0;
+            f.labels = d_labels;
+            f.lse = d_lse;
+            f.dloss = d_dloss;
+            f.dz = w.dz;
+            e = launch_few_dz(f, d_x, head, (int)dim, s);
+        } else {
+            GradArgs a{};
+            a.err = ctx->d_err;
+            a.wait_limit_ns = ctx->wait_limit_ns;
+            a.pr[0] = product(T, piece, dim, false);
+            a.pr[0].group_m = loss_group_m(dim);
+            a.T = T;
+            a.v0 = v0;
+            a.vocab = (int)vocab;
+            a.dz_chunks = (int)(piece / 64);
+            a.labels = d_labels;
+            a.lse = d_lse;
+            a.dloss = d_dloss;
+            a.dz = w.dz;
+            tm[0] = tm[2] = x_k;
+            e = make_tma_16bit(&tm[1], head, vocab - v0, dim, kBM, false);
+            if (e != cudaSuccess) break;
+            tm[3] = tm[1];
+            e = launch_grad_dz(a, tm, s);
+        }
         if (e != cudaSuccess) break;
-        tm[3] = tm[1];
-        if ((e = launch_grad_dz(a, tm, s)) != cudaSuccess) break;
         // dx += dz head, dhead = dz^T x
         GradArgs g{};
         g.err = ctx->d_err;

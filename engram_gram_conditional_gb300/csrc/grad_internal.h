@@ -52,6 +52,25 @@ int grad_pairs();  // CTA pairs of a launch that fills the device
 cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
+// ---- the loss's logits of at most kFewTokens tokens (kernels_few.cu) ----
+constexpr int kFewTokens = 64;
+struct FewArgs {
+    int T, kb;             // tokens, blocks of 64 columns
+    int rows, vocab;       // vocabulary rows of the piece, of the head
+    int64_t v0;            // first of the piece
+    const int32_t* labels;
+    const float *lse, *dloss;
+    float* zlabel;
+    float2* part;          // [few_groups(rows)][T]
+    uint16_t* dz;          // 128 x 64 tiles, one row of them; tokens 0..63 are written
+    uint32_t* err;
+    long long wait_limit_ns;
+};
+int few_groups(int64_t rows);
+cudaError_t launch_few_lse(const FewArgs& a, const uint16_t* x, const uint16_t* head, int dim, cudaStream_t s);
+// (head: its row v0)
+cudaError_t launch_few_dz(const FewArgs& a, const uint16_t* x, const uint16_t* head, int dim, cudaStream_t s);
+
 cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,
                                 const int32_t* labels, int vocab, float* loss, float* lse,
                                 uint32_t* err, cudaStream_t s);

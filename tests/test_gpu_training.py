@@ -464,7 +464,8 @@ def test_project_backward_of_no_tokens():
 # ---- loss --------------------------------------------------------------------------------------
 
 LOSS = [(1, 1, 8), (1, 257, 64), (2, 1000, 40), (129, 511, 72), (300, 3001, 264), (513, 777, 1032),
-        (64, 40_000, 128), (7, 129_280, 64)]
+        (64, 40_000, 128), (7, 129_280, 64), (16, 31, 1032), (17, 4897, 2056), (33, 130, 200),
+        (64, 6001, 4104), (65, 6001, 136)]
 
 
 def loss_problem(T, V, dim):
