@@ -197,22 +197,6 @@ __device__ __forceinline__ Heads find_heads(const uint32_t (&key)[kSortBatch], u
     }
     return h;
 }
-// Writes the segments of those places; `seg` is the number of segments before them.
-__device__ __forceinline__ void put_segments(const EmbedSort& a, const Heads& h, int64_t i0, int64_t end,
-                                             uint32_t seg) {
-#pragma unroll
-    for (int u = 0; u < kSortBatch; ++u) {
-        const int64_t i = i0 + u;
-        if (i >= end || h.key[u] >= (uint32_t)a.rows) continue;
-        if ((h.begins >> u) & 1u) {
-            a.unique[seg] = h.key[u];
-            a.seg_start[seg] = (uint32_t)i;
-            ++seg;
-        }
-        a.segpos[i] = seg - 1u;
-    }
-}
-
 // Stable radix sort of (id, position), least significant digit first, then the
 // segments of equal ids.  A block owns a contiguous range of the keys, in tiles
 // of up to 8,192, a warp a contiguous part of a tile, so the order of equal
@@ -375,9 +359,11 @@ k_embed_sort(const EmbedSort a) {
         // (hi is a multiple of eight unless it is n: `after` is the next place's key)
         return find_heads(key, before, after, i0, hi < a.n && i0 + kSortBatch >= hi ? hi + 1 : hi, rows);
     };
+    Heads h;
+    h.begins = h.last = 0;
     uint32_t heads = 0;
     for (int64_t i0 = lo + threadIdx.x * kSortBatch; i0 < hi; i0 += kSortThreads * kSortBatch) {
-        const Heads h = heads_at(i0);
+        h = heads_at(i0);
         heads += __popc(h.begins);
         if (h.last) __stcg(a.n_valid, (uint32_t)(i0 + __ffs(h.last)));
     }
@@ -408,12 +394,37 @@ k_embed_sort(const EmbedSort a) {
     uint32_t base = shared_base;
     for (int64_t t0 = lo; t0 < hi; t0 += kSortThreads * kSortBatch) {
         const int64_t i0 = t0 + threadIdx.x * kSortBatch;
-        Heads h;
-        h.begins = 0;
-        if (i0 < hi) h = heads_at(i0);
+        if (hi - lo > kSortThreads * kSortBatch) {  // (else as found above)
+            h.begins = 0;
+            if (i0 < hi) h = heads_at(i0);
+        }
         uint32_t all;
-        const uint32_t before = block_scan(__popc(h.begins), warp_sum, &all);
-        if (i0 < hi) put_segments(a, h, i0, hi, base + before);
+        uint32_t seg = block_scan(__popc(h.begins), warp_sum, &all);
+        // the segments that begin here go out through shared memory, in order
+        uint32_t pos[kSortBatch];
+        bool valid = i0 + kSortBatch <= hi;
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            if ((h.begins >> u) & 1u) tile[seg++] = make_uint2(h.key[u], (uint32_t)(i0 + u));
+            pos[u] = base + seg - 1u;
+            valid &= i0 < hi && h.key[u] < rows;
+        }
+        if (valid) {
+            uint4* p = reinterpret_cast<uint4*>(a.segpos + i0);
+            p[0] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+            p[1] = make_uint4(pos[4], pos[5], pos[6], pos[7]);
+        } else if (i0 < hi) {
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u)
+                if (i0 + u < hi && h.key[u] < rows) a.segpos[i0 + u] = pos[u];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < (int)all; i += kSortThreads) {
+            const uint2 x = tile[i];
+            a.unique[base + i] = x.x;
+            a.seg_start[base + i] = x.y;
+        }
+        __syncthreads();
         base += all;
     }
 }
