@@ -533,13 +533,14 @@ k_embed_sort_small(const EmbedSort a) {
 }
 
 // ---- sums over the segments ---------------------------------------------------------------
-// A chunk is kSumRows consecutive places of the sorted order; a group of `lanes`
-// threads sums one chunk's rows over 8 columns per thread, in order, and writes
-// each segment that begins and ends in the chunk.  A segment that crosses
-// chunks leaves one partial sum per chunk - the chunk's head (it began earlier)
-// or tail (it begins here) - for k_embed_join, which adds them in order.  So no
-// sum depends on the order in which blocks run, and a hot id's rows are spread
-// over as many threads as a cold one's.
+// A chunk is rows_per_chunk consecutive places of the sorted order; a group of
+// `lanes` threads sums one chunk's rows over 8 columns per thread, in order.  The
+// chunk in which a segment begins finishes it where at most half a chunk of it
+// lies beyond, and the next chunk starts after it.  A longer segment leaves one
+// partial sum per chunk - the chunk's head (it began earlier) or tail (it begins
+// here) - for k_embed_join, which adds them in order.  So no sum depends on the
+// order in which blocks run, and a hot id's rows are spread over as many threads
+// as a cold one's.
 constexpr int kSumBatch = 8;  // rows loaded before they are added
 
 __device__ __forceinline__ void put_row(const EmbedSum& a, uint32_t seg, int col,
@@ -571,16 +572,38 @@ k_embed_sum(const EmbedSum a) {
     const int64_t chunk = work / a.slices;
     const int col = ((int)(work - chunk * a.slices) * a.lanes + l) * 8;
     const int64_t nv = *a.n_valid;
-    const int64_t lo = chunk * a.rows_per_chunk;
+    int64_t lo = chunk * a.rows_per_chunk, hi = min(lo + a.rows_per_chunk, nv);
+    const int beyond = a.rows_per_chunk / 2;
+    bool began_before = false, goes_on = false;
+    uint32_t cur = 0u;
+    if (lo < hi) {
+        // (loads of neighbouring places and, where a segment crosses, its ends)
+        cur = a.segpos[lo];
+        const uint32_t tail = a.segpos[hi - 1];
+        began_before = lo > 0 && a.segpos[lo - 1] == cur;
+        goes_on = hi < nv && a.segpos[hi] == tail;
+        if (goes_on) {
+            const int64_t s0 = a.seg_start[tail], s1 = a.seg_start[tail + 1];
+            if (s0 >= lo && s1 - hi <= beyond) {
+                hi = s1;
+                goes_on = false;
+            }
+        }
+        if (began_before) {
+            const int64_t s0 = a.seg_start[cur], s1 = a.seg_start[cur + 1];
+            if (s0 >= lo - a.rows_per_chunk && s1 - lo <= beyond) {  // the chunk before finishes it
+                lo = s1;
+                ++cur;
+                began_before = false;
+            }
+        }
+    }
     // (a group beyond the last place, or a lane beyond dim, takes part in the
     // shuffles with nothing to add)
-    const int count = (int)max((int64_t)0, min((int64_t)a.rows_per_chunk, nv - lo));
+    const int count = (int)max((int64_t)0, hi - lo);
+    const int most = __reduce_max_sync(0xFFFFFFFFu, count);  // of the warp's groups
     const bool in = count > 0 && col < a.dim;
     float acc[8] = {};
-    uint32_t cur = count > 0 ? a.segpos[lo] : 0u;
-    const uint32_t tail = count > 0 ? a.segpos[lo + count - 1] : 0u;
-    bool began_before = count > 0 && lo > 0 && a.segpos[lo - 1] == cur;
-    const bool goes_on = count > 0 && lo + count < nv && a.segpos[lo + count] == tail;
     auto flush = [&](bool ends) {
         if (in) {
             if (ends && !began_before)
@@ -603,7 +626,7 @@ k_embed_sum(const EmbedSum a) {
     };
     uint32_t seg, row;
     place(0, seg, row);
-    for (int i0 = 0; i0 < a.rows_per_chunk; i0 += a.lanes) {
+    for (int i0 = 0; i0 < most; i0 += a.lanes) {
         uint32_t next_seg, next_row;
         place(i0 + a.lanes, next_seg, next_row);
         for (int j0 = 0; j0 < a.lanes; j0 += kPlaces) {
@@ -643,12 +666,12 @@ k_embed_sum(const EmbedSum a) {
     if (count > 0) flush(!goes_on);
 }
 
-// The rows of segments that cross chunks: a segment that begins in a chunk and
-// leaves it is that chunk's tail and the following chunks' heads, added in order.
-// A block looks at eight chunks, a warp at one: the warp adds a row of up to
-// kJoinAlone parts itself; a longer one (a hot id) is added by the block, each
-// warp a contiguous share, then the shares in order.
-constexpr int kJoinAlone = 32;
+// The rows of the segments that left partial sums: the tail of the chunk in which
+// one begins and the heads of the chunks after it, added in order.  A block looks
+// for them in `look` chunks (at most kJoinMost), then each warp takes one after the other; one
+// of more than kJoinAlone parts (a hot id) is added by the whole block, each warp
+// a contiguous share, then the shares in order.
+constexpr int kJoinMost = 64, kJoinAlone = 32;
 
 __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int64_t p0, int64_t p1, int col,
                                           float (&acc)[8]) {
@@ -662,49 +685,56 @@ __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int6
     }
 }
 
-__global__ void __launch_bounds__(256)
-k_embed_join(const EmbedSum a, int64_t chunks) {
+__global__ void __launch_bounds__(256, 3)
+k_embed_join(const EmbedSum a, int64_t chunks, int look) {
     pdl_wait();
     __shared__ float sm[8][32][9];
-    __shared__ int64_t parts_of[8];
+    __shared__ int parts_of[kJoinMost];
+    __shared__ uint32_t seg_of[kJoinMost];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = ((int)blockIdx.y * 32 + lane) * 8;
-    const int64_t nv = *a.n_valid;
-    const int64_t chunk = (int64_t)blockIdx.x * 8 + warp;
-    const int64_t lo = chunk * a.rows_per_chunk, hi = lo + a.rows_per_chunk;
-    int64_t parts = 0;
-    uint32_t seg = 0;
-    if (chunk < chunks - 1) {
-        // (three independent loads; places past nv hold nothing)
-        seg = a.segpos[hi - 1];
-        const uint32_t next = a.segpos[hi];
-        const uint32_t prev = lo ? a.segpos[lo - 1] : 0xFFFFFFFFu;
-        if (hi < nv && next == seg && prev != seg)
-            parts = ((int64_t)a.seg_start[seg + 1] - 1) / a.rows_per_chunk - chunk + 1;  // tail, heads
+    const int64_t first = (int64_t)blockIdx.x * look;
+    if ((int)threadIdx.x < look) {
+        const int64_t nv = *a.n_valid;
+        const int64_t chunk = first + threadIdx.x;
+        const int64_t lo = chunk * a.rows_per_chunk, hi = lo + a.rows_per_chunk;
+        int parts = 0;
+        uint32_t seg = 0;
+        if (chunk < chunks - 1) {
+            // (three independent loads; places past nv hold nothing)
+            seg = a.segpos[hi - 1];
+            const uint32_t next = a.segpos[hi];
+            const uint32_t prev = lo ? a.segpos[lo - 1] : 0xFFFFFFFFu;
+            if (hi < nv && next == seg && prev != seg) {
+                const int64_t s1 = a.seg_start[seg + 1];
+                if (s1 - hi > a.rows_per_chunk / 2)
+                    parts = (int)((s1 - 1) / a.rows_per_chunk - chunk + 1);  // tail, heads
+            }
+        }
+        parts_of[threadIdx.x] = parts;
+        seg_of[threadIdx.x] = seg;
     }
-    if (parts && parts <= kJoinAlone && col < a.dim) {
+    __syncthreads();
+    for (int c = warp; c < look; c += 8) {
+        const int parts = parts_of[c];
+        if (parts == 0 || parts > kJoinAlone || col >= a.dim) continue;
         float acc[8] = {};
-        add_parts(a, chunk, 0, parts, col, acc);
-        put_row(a, seg, col, acc);
+        add_parts(a, first + c, 0, parts, col, acc);
+        put_row(a, seg_of[c], col, acc);
     }
-    if (lane == 0) parts_of[warp] = parts > kJoinAlone ? parts : 0;
-    if (!__syncthreads_or(parts > kJoinAlone)) return;
-    for (int w = 0; w < 8; ++w) {
-        const int64_t all = parts_of[w];
-        if (!all) continue;
+    for (int c = 0; c < look; ++c) {
+        const int64_t parts = parts_of[c];
+        if (parts <= kJoinAlone) continue;
         float acc[8] = {};
-        add_parts(a, (int64_t)blockIdx.x * 8 + w, all * warp / 8, all * (warp + 1) / 8, col, acc);
+        add_parts(a, first + c, parts * warp / 8, parts * (warp + 1) / 8, col, acc);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sm[warp][lane][j] = acc[j];
         __syncthreads();
-        if (warp == w && col < a.dim) {
-            float sum[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] = sm[0][lane][j];
+        if (warp == 0 && col < a.dim) {
             for (int x = 1; x < 8; ++x)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] += sm[x][lane][j];
-            put_row(a, seg, col, sum);
+                for (int j = 0; j < 8; ++j) acc[j] += sm[x][lane][j];
+            put_row(a, seg_of[c], col, acc);
         }
         __syncthreads();
     }
@@ -1871,8 +1901,11 @@ cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
                              : k_embed_sum<8>;
     cudaError_t e = pdl_launch(f, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
     if (e != cudaSuccess || chunks < 2) return e;
-    return pdl_launch(k_embed_join, dim3((unsigned)((chunks + 6) / 8), (unsigned)((a.dim + 255) / 256)),
-                      dim3(256), 0, s, a, chunks);
+    // about four blocks per SM
+    const int64_t slices = (a.dim + 255) / 256, want = chunks * slices / (device_sm_count() * 4) + 1;
+    const int look = (int)std::min<int64_t>(kJoinMost, std::max<int64_t>(8, want));
+    return pdl_launch(k_embed_join, dim3((unsigned)((chunks + look - 1) / look), (unsigned)slices), dim3(256), 0, s,
+                      a, chunks, look);
 }
 
 cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t s) {
