@@ -130,6 +130,14 @@ engram_status gate_backward_call(const engram_ctx* ctx, GateTrain& a, int saved,
 
 // ---- products ----------------------------------------------------------------------------
 
+GradArgs grad_args(const engram_ctx* ctx) {
+    GradArgs a{};
+    a.err = ctx->d_err;
+    a.wait_limit_ns = ctx->wait_limit_ns;
+    a.starve = ctx->starve_b;
+    return a;
+}
+
 // One of the two gradient products of a launch.
 GradProblem product(int64_t M, int64_t N, int64_t reduce, bool a_mn) {
     GradProblem q{};
@@ -203,6 +211,7 @@ FewArgs few_args(const engram_ctx* ctx, int64_t T, uint32_t vocab, uint32_t dim)
     f.vocab = (int)vocab;
     f.err = ctx->d_err;
     f.wait_limit_ns = ctx->wait_limit_ns;
+    f.starve = ctx->starve_b;
     return f;
 }
 
@@ -222,14 +231,16 @@ GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece) {
     q.a_tiled = (int)(piece / 64);
     return q;
 }
-LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim) {
+LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim, bool want_dhead) {
     const int64_t piece = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
     const GradProblem dx = loss_dx(T, dim, piece), dh = loss_dhead(T, dim, piece, piece);
     LossBackWs w{};
-    w.splits = long_splits(dx, &dh);
+    // with and without the other product the cut may differ: room for either
+    w.splits = long_splits(dx, want_dhead ? &dh : nullptr);
+    const int most = std::max(w.splits, long_splits(dx, want_dhead ? nullptr : &dh));
     Carver c(p);
     w.dz = c.take<uint16_t>((size_t)rows * piece);
-    w.acc = c.take<float>(w.splits > 1 || piece < vocab ? (size_t)w.splits * T * dim : 0);
+    w.acc = c.take<float>(most > 1 || piece < vocab ? (size_t)most * T * dim : 0);
     w.bytes = c.bytes();
     return w;
 }
@@ -438,9 +449,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
         return fail(ENGRAM_EINVAL, "emb / dkv (16-byte aligned)");
     if (!d_demb && !d_dwkv) return ok();
     const LayerState& L = ctx->layers[layer];
-    GradArgs a{};
-    a.err = ctx->d_err;
-    a.wait_limit_ns = ctx->wait_limit_ns;
+    GradArgs a = grad_args(ctx);
     CUtensorMap tm[4];
     cudaError_t e = cudaSuccess;
     if (d_dwkv) {
@@ -504,9 +513,7 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
         f.part = part;
         e = launch_few_lse(f, d_x, d_head, (int)dim, s);
     } else {
-        GradArgs a{};
-        a.err = ctx->d_err;
-        a.wait_limit_ns = ctx->wait_limit_ns;
+        GradArgs a = grad_args(ctx);
         a.pr[0] = product(T, vocab, dim, false);
         a.pr[0].group_m = loss_group_m(dim);
         a.T = T;
@@ -529,7 +536,7 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
 
 size_t engram_loss_backward_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
     if (check_loss(vocab, dim, T) || T == 0) return 0;
-    return loss_backward_ws(nullptr, T, vocab, dim).bytes;
+    return loss_backward_ws(nullptr, T, vocab, dim, true).bytes;
 }
 
 engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
@@ -551,7 +558,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         return fail(ENGRAM_EINVAL, "x / head / workspace (16-byte aligned) / labels / lse / dloss");
     if (!d_dx && !d_dhead) return ok();
     if ((st = train_device(ctx))) return st;
-    const LossBackWs w = loss_backward_ws(d_workspace, T, vocab, dim);
+    const LossBackWs w = loss_backward_ws(d_workspace, T, vocab, dim, d_dhead != nullptr);
     const int64_t step = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
     CUtensorMap x_k, x_mn;
     cudaError_t e = make_tma_16bit(&x_k, d_x, T, dim, kBM, false);
@@ -573,9 +580,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
             f.dz = w.dz;
             e = launch_few_dz(f, d_x, head, (int)dim, s);
         } else {
-            GradArgs a{};
-            a.err = ctx->d_err;
-            a.wait_limit_ns = ctx->wait_limit_ns;
+            GradArgs a = grad_args(ctx);
             a.pr[0] = product(T, piece, dim, false);
             a.pr[0].group_m = loss_group_m(dim);
             a.T = T;
@@ -594,9 +599,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         }
         if (e != cudaSuccess) break;
         // dx += dz head, dhead = dz^T x
-        GradArgs g{};
-        g.err = ctx->d_err;
-        g.wait_limit_ns = ctx->wait_limit_ns;
+        GradArgs g = grad_args(ctx);
         const uint64_t dz_rows = (uint64_t)rows * piece / 64;
         e = make_tma_16bit(&tm[0], w.dz, dz_rows, 64, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], head, vocab - v0, dim, 64, false);

@@ -36,6 +36,7 @@ struct GradArgs {
     int pairs_more, rounds_fewer;  // how the items are dealt (set by the launcher)
     uint32_t* err;
     long long wait_limit_ns;
+    int starve;            // test hook: no operand is loaded
     // softmax epilogues
     int64_t T, v0;         // rows; first vocabulary column of the piece
     int vocab, dz_chunks;  // 64-column chunks of the piece
@@ -65,6 +66,7 @@ struct FewArgs {
     uint16_t* dz;          // 128 x 64 tiles, one row of them; tokens 0..63 are written
     uint32_t* err;
     long long wait_limit_ns;
+    int starve;
 };
 int few_groups(int64_t rows);
 cudaError_t launch_few_lse(const FewArgs& a, const uint16_t* x, const uint16_t* head, int dim, cudaStream_t s);

@@ -123,7 +123,7 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
     if (warp == kWarpTma) {
         if (lane == 0) {
             int it = 0;
-            bool ok = true;
+            bool ok = !a.starve;
             for (int i = 0; i < tiles && ok; ++i) {
                 const int row = r0 + i * kBM, n = min(kBM, r1 - row);  // n: a multiple of 32
                 for (int kb = 0; kb < kb_all; ++kb, ++it) {

@@ -241,7 +241,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
     if (warp == kWarpTma) {
         if (lane == 0) {
             int it = 0;
-            bool ok = true;
+            bool ok = !a.starve;
             for (int i = 0; i < n_items && ok; ++i) {
                 const Item w = get_item(a, pair, pairs, n_long, i);
                 const GradProblem& q = a.pr[w.pr];

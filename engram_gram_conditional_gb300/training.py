@@ -1,0 +1,110 @@
+"""One training step of a model around an Engram layer.
+
+Token embedding -> hyper-connection branches -> Engram layer -> mean of the
+branches -> output head -> cross entropy, and back, through the library's
+operators:
+
+  engram_embed              branches from the token embedding
+  engram_hash, engram_gather_dequant, engram_prepass
+                            rows, their 6,144-vectors, kv
+  engram_gate_checkpoint    the gate, its activations kept in 8 bits
+  engram_loss               loss and lse, no logits
+  engram_loss_backward      gradients of the head and of its input
+  engram_gate_backward_checkpoint, engram_project_backward
+                            gradients of the norm weights, wkv and the rows
+  engram_embed_grad         gradients of the token embedding and the n-gram table,
+                            summed over equal ids
+
+torch only allocates, and takes the mean of the branches and its transpose (the
+model around the layer).
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import (EMBED_BF16, KV_BF16, KV_F32, engram_embed, engram_embed_grad,
+               engram_embed_grad_workspace_bytes, engram_forward_staged_workspace_bytes,
+               engram_gate_backward_checkpoint, engram_gate_backward_workspace_bytes,
+               engram_gate_checkpoint, engram_gather_dequant, engram_hash, engram_loss,
+               engram_loss_backward, engram_loss_backward_workspace_bytes,
+               engram_loss_workspace_bytes, engram_prepass, engram_project_backward,
+               engram_project_backward_workspace_bytes)
+
+
+class TrainStep:
+    """Buffers and calls of one step for up to ``tokens`` tokens.
+
+    ``model``: an EngramLayerSet with ``layer`` bound; ``embedding`` and ``head``:
+    BF16 [vocab][d].  ``kv_format``: how kv waits for the gate (KV_F32 or KV_BF16).
+    """
+
+    def __init__(self, model, layer: int, embedding, head, tokens: int, *, kv_format=KV_BF16,
+                 scale=None):
+        g = model.geom
+        self.model, self.layer, self.embedding, self.head = model, layer, embedding, head
+        self.vocab, self.d, self.hc = embedding.shape[0], g["d"], g["hc"]
+        self.kv_format, self.scale = kv_format, math.sqrt(g["d"]) if scale is None else scale
+        self.tokens = tokens
+        T, nb, K, N, kept = tokens, model.nb, model.K, model.N, (2 * self.hc + 1) * self.d
+        bf16, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+
+        def new(*shape, dtype=bf16):
+            return torch.empty(*shape, dtype=dtype, device=model.device)
+
+        self.hidden, self.out = new(T, self.hc, self.d), new(T, self.hc, self.d)
+        self.rows, self.emb = new(T, nb, dtype=i32), new(T, K)
+        self.kv = new(T, N, dtype=f32 if kv_format == KV_F32 else bf16)
+        self.gates = new(T, self.hc, dtype=f32)
+        self.codes, self.scales = new(T, kept, dtype=u8), new(T, kept // 32, dtype=u8)
+        self.loss, self.lse = new(T, dtype=f32), new(T, dtype=f32)
+        self.dx, self.dhead = new(T, self.d), new(self.vocab, self.d)
+        self.dhidden, self.dkv = new(T, self.hc, self.d), new(T, N)
+        self.dwq, self.dwk = new(self.hc, self.d, dtype=f32), new(self.hc, self.d, dtype=f32)
+        self.demb, self.dwkv = new(T, K), new(N, K)
+        self.token_ids, self.token_count = new(T, dtype=i32), new(1, dtype=i32)
+        self.token_grad = new(T, self.d, dtype=f32)
+        self.row_ids, self.row_count = new(T * nb, dtype=i32), new(1, dtype=i32)
+        self.row_grad = new(T * nb, g["row_dim"], dtype=f32)
+        ctx = model.ctx
+        self.ws = new(max(engram_forward_staged_workspace_bytes(ctx, T),
+                          engram_loss_workspace_bytes(T, self.vocab, self.d),
+                          engram_loss_backward_workspace_bytes(T, self.vocab, self.d),
+                          engram_gate_backward_workspace_bytes(ctx, T),
+                          engram_project_backward_workspace_bytes(ctx, T),
+                          engram_embed_grad_workspace_bytes(T, self.vocab, self.d),
+                          engram_embed_grad_workspace_bytes(T * nb, model.rows(layer),
+                                                            g["row_dim"]), 16), dtype=u8)
+
+    def forward(self, ids, windows, labels, stream=None):
+        """Loss of each token (fp32 [T]); ids and labels int32 [T], windows int32 [T][4] (an
+        image row has slot 0 DEAD), all on the device."""
+        ctx, layer, T = self.model.ctx, self.layer, self.tokens
+        engram_embed(ctx, self.embedding, EMBED_BF16, self.vocab, self.d, ids, T, self.scale, self.hc,
+                     self.hidden, stream)
+        engram_hash(ctx, layer, windows, T, self.rows, stream)
+        engram_gather_dequant(ctx, layer, self.rows, T, self.emb, stream)
+        engram_prepass(ctx, layer, windows, T, self.kv, self.kv_format, self.ws, stream)
+        engram_gate_checkpoint(ctx, layer, self.kv, self.kv_format, windows, T, self.hidden, self.out,
+                               self.gates, self.codes, self.scales, stream)
+        self.x = self.out.float().mean(1).bfloat16()
+        engram_loss(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.loss, self.lse, self.ws,
+                    stream)
+        return self.loss
+
+    def backward(self, ids, windows, labels, dloss, stream=None):
+        """Gradients of sum(dloss * loss) (dloss fp32 [T]) into this object's buffers: dhead, dwq,
+        dwk, dwkv, and the sparse token_ids/token_grad and row_ids/row_grad with their counts."""
+        ctx, layer, T = self.model.ctx, self.layer, self.tokens
+        engram_loss_backward(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.lse, dloss,
+                             self.dx, self.dhead, self.ws, stream)
+        dout = (self.dx.float() / self.hc).bfloat16().unsqueeze(1).expand(-1, self.hc, -1).contiguous()
+        engram_gate_backward_checkpoint(ctx, layer, self.codes, self.scales, windows, T, dout,
+                                        self.dhidden, self.dkv, self.dwq, self.dwk, self.ws, stream)
+        engram_project_backward(ctx, layer, self.emb, self.dkv, T, self.demb, self.dwkv, self.ws, stream)
+        engram_embed_grad(ctx, self.vocab, self.d, ids, T, self.scale, self.hc, self.dhidden,
+                          self.token_ids, self.token_count, self.token_grad, 0, self.ws, stream)
+        row_dim = self.model.geom["row_dim"]
+        engram_embed_grad(ctx, self.model.rows(layer), row_dim, self.rows, T * self.model.nb, 1.0, 1,
+                          self.demb, self.row_ids, self.row_count, self.row_grad, 0, self.ws, stream)

@@ -585,8 +585,9 @@ engram_status engram_sync(const engram_ctx* ctx, void* stream);
  * engram_sync reports ENGRAM_ETIMEOUT and the context stays usable. */
 engram_status engram_ctx_set_wait_limit(engram_ctx* ctx, int64_t ns);
 /* Test hook for the bounded waits: while on, the GEMM kernels issue no wkv
- * loads, so the tensor-core issuer's wait for them runs out (after the wait
- * limit) and the call ends with ENGRAM_ETIMEOUT.  Nothing faults or hangs. */
+ * loads (the training products and the loss: no loads at all), so the
+ * tensor-core issuer's wait for them runs out (after the wait limit) and the
+ * call ends with ENGRAM_ETIMEOUT.  Nothing faults or hangs. */
 engram_status engram_debug_starve_operand(engram_ctx* ctx, int on);
 
 /* Message of the calling thread's last error ("" if none). */

@@ -610,3 +610,77 @@ def test_operators_run_on_their_own_stream(plain_ctx):
     eg.engram_sync(plain_ctx, st)
     _, rlse, _ = loss_ref(x, head, y)
     assert (lse.cpu().to(F) - rlse).abs().max() <= 1e-3
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_context_stays_usable():
+    s = make_layer()
+    V, dim = 2000, 256
+    try:
+        for T in (10, 100):
+            x, head, y = (t.cuda() for t in loss_problem(T, V, dim))
+            loss, lse = (torch.empty(T, device="cuda") for _ in range(2))
+            ws = ws_of(eg.engram_loss_workspace_bytes(T, V, dim))
+            eg.engram_ctx_set_wait_limit(s.ctx, 20_000_000)
+            eg.engram_debug_starve_operand(s.ctx, True)
+            eg.engram_loss(s.ctx, x, head, V, dim, y, T, loss, lse, ws)
+            with pytest.raises(eg.EngramError) as e:
+                eg.engram_sync(s.ctx)
+            assert e.value.status == eg.ETIMEOUT
+            eg.engram_debug_starve_operand(s.ctx, False)
+            eg.engram_ctx_set_wait_limit(s.ctx, 4_000_000_000)
+            eg.engram_loss(s.ctx, x, head, V, dim, y, T, loss, lse, ws)
+            eg.engram_sync(s.ctx)
+            _, rlse, _ = loss_ref(x.cpu(), head.cpu(), y.cpu())
+            assert (lse.cpu().to(F) - rlse).abs().max() <= 1e-3
+    finally:
+        s.close()
+
+
+def test_operators_in_a_captured_graph(plain_ctx):
+    """Captured once, replayed on new inputs in the same buffers."""
+    n, rows, dim, T, V = 20_000, 3000, 64, 100, 1500
+    ids, dout = ids_like("zipf", n, rows, 1).cuda(), rnd(2, n, 1, dim).cuda()
+    x, head, y = (t.cuda() for t in loss_problem(T, V, dim))
+    grad = torch.zeros(rows, dim, device="cuda")
+    loss, lse = (torch.empty(T, device="cuda") for _ in range(2))
+    dx, dhead = torch.empty_like(x), torch.empty_like(head)
+    dloss = torch.ones(T, device="cuda")
+    ws1 = ws_of(eg.engram_embed_grad_workspace_bytes(n, rows, dim))
+    ws2 = ws_of(max(eg.engram_loss_workspace_bytes(T, V, dim),
+                    eg.engram_loss_backward_workspace_bytes(T, V, dim)))
+
+    def calls(st):
+        eg.engram_embed_grad(plain_ctx, rows, dim, ids, n, 1.0, 1, dout, None, None, grad, 0, ws1, st)
+        eg.engram_loss(plain_ctx, x, head, V, dim, y, T, loss, lse, ws2, st)
+        eg.engram_loss_backward(plain_ctx, x, head, V, dim, y, T, lse, dloss, dx, dhead, ws2, st)
+
+    calls(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(torch.cuda.current_stream())
+    for k in (3, 4):
+        ids.copy_(ids_like("zipf", n, rows, k))
+        dout.copy_(rnd(k, n, 1, dim))
+        x.copy_(rnd(k, T, dim))
+        graph.replay()
+        eg.engram_sync(plain_ctx, torch.cuda.current_stream())
+        got = [t.clone() for t in (grad, loss, lse, dx, dhead)]
+        calls(None)
+        torch.cuda.synchronize()
+        for a, b in zip(got, (grad, loss, lse, dx, dhead)):
+            assert torch.equal(a, b)
+
+
+def test_training_example_learns():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "train_engram.py")
+    spec = importlib.util.spec_from_file_location("train_engram", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.run(steps=20)
+    assert all(math.isfinite(x) for x in losses)
+    assert losses[-1] < losses[0] - 0.5
