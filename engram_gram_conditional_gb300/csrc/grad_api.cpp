@@ -475,7 +475,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
     if (!d_dwkv) tm[2] = tm[0], tm[3] = tm[1];
     e = launch_grad_products(a, tm, s);
     if (e == cudaSuccess && a.pr[0].acc_write)
-        e = launch_sum_splits(a.pr[0].acc, a.pr[0].splits, T * K, d_demb, s);
+        e = launch_sum_splits(a.pr[0].acc, a.pr[0].splits, T * K, nullptr, d_demb, s);
     if (e != cudaSuccess) return cuda_fail(e, "project backward launch");
     return ok();
 }
@@ -600,6 +600,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         if (e != cudaSuccess) break;
         // dx += dz head, dhead = dz^T x
         GradArgs g = grad_args(ctx);
+        g.unit = d_dloss;
         const uint64_t dz_rows = (uint64_t)rows * piece / 64;
         e = make_tma_16bit(&tm[0], w.dz, dz_rows, 64, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], head, vocab - v0, dim, 64, false);
@@ -621,7 +622,7 @@ engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const u
         e = launch_grad_products(g, tm, s);
     }
     if (e == cudaSuccess && d_dx && w.splits > 1)
-        e = launch_sum_splits(w.acc, w.splits, T * (int64_t)dim, d_dx, s);
+        e = launch_sum_splits(w.acc, w.splits, T * (int64_t)dim, d_dloss, d_dx, s);
     if (e != cudaSuccess) return cuda_fail(e, "loss backward launch");
     return ok();
 }

@@ -12,6 +12,18 @@ enum GradEpilogue : int {
     kGradOut = 2,  // a product's output
 };
 
+// The loss's dz is kept as (exp(z - lse) - [v = label]) dloss[t] / unit, and the
+// products are multiplied by the unit: with equal weights, the usual case, the
+// large term of every row is then close to -1 and rounds almost exactly, where
+// -1 / T (every row with the same error of up to 2^-8) would scale the whole
+// gradient.
+#ifdef __CUDACC__
+__device__ __forceinline__ float loss_unit(const float* dloss) {
+    const float u = dloss[0], size = fabsf(u);
+    return size >= 0x1p-30f && size <= 0x1p30f ? u : 1.0f;
+}
+#endif
+
 struct FastDiv {
     uint32_t d, m, s;  // divisor, multiplier, shift
 };
@@ -37,6 +49,7 @@ struct GradArgs {
     uint32_t* err;
     long long wait_limit_ns;
     int starve;            // test hook: no operand is loaded
+    const float* unit;     // kGradOut: outputs are multiplied by loss_unit(unit); null: by 1
     // softmax epilogues
     int64_t T, v0;         // rows; first vocabulary column of the piece
     int vocab, dz_chunks;  // 64-column chunks of the piece
@@ -76,8 +89,8 @@ cudaError_t launch_few_dz(const FewArgs& a, const uint16_t* x, const uint16_t* h
 cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,
                                 const int32_t* labels, int vocab, float* loss, float* lse,
                                 uint32_t* err, cudaStream_t s);
-cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, uint16_t* out,
-                              cudaStream_t s);
+cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, const float* unit,
+                              uint16_t* out, cudaStream_t s);
 
 
 // ---- embedding (kernels_train.cu) ----

@@ -220,6 +220,7 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
             const bool in = row < r1 && v < a.vocab;
             if constexpr (kDz) {
                 if (row >= r1) continue;  // (uniform in the warp: ranges are multiples of 32)
+                const float unit = loss_unit(a.dloss);
                 uint16_t* out = a.dz + (int64_t)(row >> 6) * (128 * 64) + (row & 63);
 #pragma unroll
                 for (int t = 0; t < kN; ++t) {
@@ -230,7 +231,7 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
                         // (z - lse first: exact where p is near 1)
                         float p = exp2f((z[t] - a.lse[t]) * kLog2e);
                         if (label == v) p -= 1.f;
-                        if (in && label >= 0 && label < a.vocab) d = p * a.dloss[t];
+                        if (in && label >= 0 && label < a.vocab) d = p * (a.dloss[t] / unit);
                     }
                     out[t * 64] = (uint16_t)(bf16x2_pack_rn(d, d) & 0xFFFFu);
                 }

@@ -335,6 +335,8 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
         const int q4 = warp & 3, grp = warp >> 2;  // TMEM quadrant; columns [kCols grp, kCols grp + kCols)
         const int m = q4 * 32 + lane;
         const uint32_t box = sbase + L::kOffOut + (uint32_t)(warp * kBox);
+        const float unit = kEpi == kGradDz ? loss_unit(a.dloss)
+                           : kEpi == kGradOut && a.unit ? loss_unit(a.unit) : 1.0f;
         int use = 0;  // accumulators used so far
         auto acc_ready = [&]() {
             const int acc = use & 1;
@@ -367,7 +369,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                     if (label >= a.vocab) label = -1;
                     if (kEpi == kGradDz) {
                         lse = a.lse[row];
-                        dl = label >= 0 ? a.dloss[row] : 0.f;
+                        dl = label >= 0 ? a.dloss[row] / unit : 0.f;
                     }
                 }
             }
@@ -477,8 +479,8 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             o[c + j / 16][j % 16] =
-                                bf16x2_pack_rn(__uint_as_float(r[j / 16][2 * (j % 16)]),
-                                               __uint_as_float(r[j / 16][2 * (j % 16) + 1]));
+                                bf16x2_pack_rn(__uint_as_float(r[j / 16][2 * (j % 16)]) * unit,
+                                               __uint_as_float(r[j / 16][2 * (j % 16) + 1]) * unit);
                     }
                     acc_done();
 #pragma unroll
@@ -524,8 +526,10 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                             }
                             if (!q.acc_write)
                                 st_shared_v4(out_piece(box, lane, c * 4 + j / 8),
-                                             make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
-                                                        bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7])));
+                                             make_uint4(bf16x2_pack_rn(v[0] * unit, v[1] * unit),
+                                                        bf16x2_pack_rn(v[2] * unit, v[3] * unit),
+                                                        bf16x2_pack_rn(v[4] * unit, v[5] * unit),
+                                                        bf16x2_pack_rn(v[6] * unit, v[7] * unit)));
                         }
                     }
                     __syncwarp();
@@ -594,10 +598,11 @@ __global__ void k_loss_combine(const float2* part, int groups, int64_t T, const 
     if (loss) loss[t] = y >= 0 && y < vocab ? l - zlabel[t] : 0.f;
 }
 
-// out = the sum of the splits' fp32 buffers, in order, rounded to BF16 (n a
-// multiple of 8).
-__global__ void k_sum_splits(const float* acc, int splits, int64_t n, uint16_t* out) {
+// out = the sum of the splits' fp32 buffers, in order, times the unit, rounded to
+// BF16 (n a multiple of 8).
+__global__ void k_sum_splits(const float* acc, int splits, int64_t n, const float* unit, uint16_t* out) {
     pdl_wait();
+    const float by = unit ? loss_unit(unit) : 1.0f;
     const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8;
     if (i >= n) return;
     float v[8] = {};
@@ -607,6 +612,8 @@ __global__ void k_sum_splits(const float* acc, int splits, int64_t n, uint16_t* 
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= by;
     *reinterpret_cast<uint4*>(out + i) =
         make_uint4(bf16x2_pack_rn(v[0], v[1]), bf16x2_pack_rn(v[2], v[3]),
                    bf16x2_pack_rn(v[4], v[5]), bf16x2_pack_rn(v[6], v[7]));
@@ -738,9 +745,9 @@ cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const
     return pdl_launch((void*)k_loss_combine, dim3((unsigned)((T + 31) / 32)), dim3(256), args, s);
 }
 
-cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, uint16_t* out,
+cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, const float* unit, uint16_t* out,
                               cudaStream_t s) {
-    void* args[] = {&acc, &splits, &n, &out};
+    void* args[] = {&acc, &splits, &n, &unit, &out};
     return pdl_launch((void*)k_sum_splits, dim3((unsigned)((n / 8 + 255) / 256)), dim3(256), args, s);
 }
 

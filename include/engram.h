@@ -562,9 +562,9 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
                           float* d_loss, float* d_lse, void* d_workspace, void* stream);
 /* Its gradient, in pieces of the vocabulary: the logits of a piece are computed
  * again, dz = (exp(z - lse) - [v = label]) dloss[t] (0 where the label is
- * ignored) is kept as BF16 for that piece only, and dx = dz head (bf16
- * [T][dim]) and dhead = dz^T x (bf16 [vocab][dim], written) are summed in fp32
- * and rounded once.  d_lse: engram_loss's; d_dloss fp32 [T]; d_dx or d_dhead
+ * ignored) is kept as BF16, in units of dloss[0], for that piece only, and dx =
+ * dz head (bf16 [T][dim]) and dhead = dz^T x (bf16 [vocab][dim], written) are
+ * summed in fp32 and rounded once.  d_lse: engram_loss's; d_dloss fp32 [T]; d_dx or d_dhead
  * may be NULL.  d_workspace: engram_loss_backward_workspace_bytes(T, vocab, dim)
  * bytes: the piece's dz (about 64 MB, 8 KB per token for a very long batch)
  * and the fp32 dx. */

@@ -529,6 +529,34 @@ def test_loss_backward(plain_ctx, T, V, dim, want):
         assert ((got.cpu().to(F) - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("T", [3, 60, 300, 700])
+def test_loss_backward_of_equal_weights_is_not_scaled(plain_ctx, T):
+    """With weights of 1 / T for a T that is no power of two, BF16 rounding of dz must not scale
+    the gradient: its projection on the exact one is 1 to within what independent roundings of
+    at most 2^-8 give over its elements (2^-8 / sqrt(T)), and the probabilities' size."""
+    V, dim = 3000, 128
+    x, head, y = loss_problem(T, V, dim)
+    y = y.clamp_min(0)
+    dloss = torch.full((T,), 1.0 / T)
+    lse = torch.empty(T, device="cuda")
+    ws = ws_of(max(eg.engram_loss_workspace_bytes(T, V, dim),
+                   eg.engram_loss_backward_workspace_bytes(T, V, dim)))
+    dev = [t.cuda() for t in (x, head, y, dloss)]
+    eg.engram_loss(plain_ctx, dev[0], dev[1], V, dim, dev[2], T, None, lse, ws)
+    dx = torch.empty(T, dim, dtype=torch.bfloat16, device="cuda")
+    dhead = torch.empty(V, dim, dtype=torch.bfloat16, device="cuda")
+    eg.engram_loss_backward(plain_ctx, dev[0], dev[1], V, dim, dev[2], T, lse, dev[3], dx, dhead, ws)
+    eg.engram_sync(plain_ctx)
+    z, rlse, _ = loss_ref(x, head, y)
+    dz = torch.exp(z - rlse.unsqueeze(1))
+    p = dz[torch.arange(T), y.long()].clone()
+    dz[torch.arange(T), y.long()] -= 1
+    dz *= dloss.to(F).unsqueeze(1)
+    for got, ref in ((dx, dz @ head.to(F)), (dhead, dz.T @ x.to(F))):
+        along = float((got.cpu().to(F) * ref).sum() / (ref * ref).sum())
+        assert abs(along - 1) <= 2.0 ** -8 / math.sqrt(T) + float(p.mean()), along
+
+
 def test_loss_backward_against_differences(plain_ctx):
     T, V, dim = 5, 70, 16
     x, head, y = loss_problem(T, V, dim)
