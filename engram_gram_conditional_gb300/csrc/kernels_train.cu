@@ -85,7 +85,7 @@ k_embed(const void* __restrict__ table, uint64_t rows, int dim, const uint32_t* 
 // ---- sort of the ids -------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kSortBatch = 8;  // rounds of 32 keys that a warp loads at once
-constexpr int kSmallSort = kSortThreads * 8;  // keys of the one-cluster sort
+constexpr int kSmallSort = kSortThreads * 8 * 4;  // keys of the one-cluster sort
 
 // A barrier of the cooperative launch's blocks in two halves, so that a block can
 // work between them; the wait is bounded: false on a time-out.
@@ -429,14 +429,16 @@ k_embed_sort(const EmbedSort a) {
     }
 }
 
-// The same sort for at most kSmallSort ids by one cluster, a key per thread: the
-// keys move between the CTAs' shared memories, no pass touches global memory.
-// (One block with eight keys a thread took 27 us for 8,192 ids, bound by its
-// issue rate.)
+// The same sort for at most kSmallSort ids by one cluster of up to eight CTAs,
+// kPer keys a thread: the keys move between the CTAs' shared memories, no pass
+// touches global memory, and the cluster's barrier takes the grid's place.  (One
+// block with eight keys a thread took 27 us for 8,192 ids, bound by its issue
+// rate, a cluster with one 15.)
+template <int kPer>
 __global__ void __launch_bounds__(kSortThreads)
 k_embed_sort_small(const EmbedSort a) {
-    extern __shared__ uint32_t cnt[];  // [kSortWarps][bins]
-    __shared__ uint32_t keys[2][kSortThreads], vals[2][kSortThreads];
+    constexpr int kKeys = kSortThreads * kPer;  // of a CTA
+    extern __shared__ uint32_t cnt[];           // [kSortWarps][bins], then pairs [2][kKeys]
     __shared__ uint32_t totals[512];
     __shared__ uint32_t warp_sum[kSortWarps];
     __shared__ uint32_t edge[3];  // first and last key, segments that begin here
@@ -445,15 +447,21 @@ k_embed_sort_small(const EmbedSort a) {
     const uint32_t rank = cluster_ctarank(), cs = gridDim.x;
     const int n = (int)a.n, bins = 1 << a.digit_bits;
     const uint32_t dmask = (uint32_t)bins - 1u, rows = (uint32_t)a.rows;
+    uint2* const pairs = reinterpret_cast<uint2*>(cnt + kSortWarps * bins);
     pdl_wait();
     pdl_launch_dependents();
-    const int i = (int)rank * kSortThreads + (int)threadIdx.x;
-    // keys beyond n are larger than any: they stay behind
-    uint32_t k = 0xFFFFFFFFu, v = (uint32_t)i;
-    if (i < n) {
-        const uint32_t id = a.ids[i];
-        k = min(id, rows);
-        if (id >= rows && id != kMasked) atomicOr(a.err, kErrBounds);
+    const int own = warp * 32 * kPer + lane;  // this thread's first key within the CTA, then every 32nd
+    uint2 kv[kPer];
+    uint32_t same[kPer], at[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int i = (int)rank * kKeys + own + 32 * u;
+        kv[u] = make_uint2(0xFFFFFFFFu, (uint32_t)i);  // keys beyond n are larger than any: they stay behind
+        if (i < n) {
+            const uint32_t id = a.ids[i];
+            kv[u].x = min(id, rows);
+            if (id >= rows && id != kMasked) atomicOr(a.err, kErrBounds);
+        }
     }
     uint32_t* const mine = cnt + warp * bins;
     auto remote = [&](const uint32_t* p, uint32_t r) {
@@ -462,11 +470,18 @@ k_embed_sort_small(const EmbedSort a) {
         return x;
     };
     for (int pass = 0; pass < a.passes; ++pass) {
-        const uint32_t d = (k >> (pass * a.digit_bits)) & dmask;
+        const int shift = pass * a.digit_bits, to = pass & 1;
         for (int x = lane; x < bins; x += 32) mine[x] = 0;
         __syncwarp();
-        const uint32_t same = same_digit(d, a.digit_bits, 0xFFFFFFFFu);
-        if ((same & lt) == 0u) mine[d] = __popc(same);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const uint32_t d = (kv[u].x >> shift) & dmask;
+            same[u] = same_digit(d, a.digit_bits, 0xFFFFFFFFu);
+            at[u] = mine[d] + __popc(same[u] & lt);
+            __syncwarp();
+            if ((same[u] & lt) == 0u) mine[d] += __popc(same[u]);
+            __syncwarp();
+        }
         __syncthreads();
         const uint32_t total = scan_warps(cnt, bins);
         if ((int)threadIdx.x < bins) totals[threadIdx.x] = total;
@@ -482,30 +497,42 @@ k_embed_sort_small(const EmbedSort a) {
         const uint32_t base = block_scan(sum, warp_sum, &all);
         add_warps(cnt, bins, base + before);
         __syncthreads();
-        const uint32_t p = mine[d] + __popc(same & lt);
-        const int to = pass & 1;
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(keys[to] + (p & 1023u)), p >> 10)),
-                     "r"(k)
-                     : "memory");
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(vals[to] + (p & 1023u)), p >> 10)),
-                     "r"(v)
-                     : "memory");
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const uint32_t p = at[u] + mine[(kv[u].x >> shift) & dmask];
+            const uint32_t dst = map_rank(smem_u32(pairs + to * kKeys + (p & (kKeys - 1))), p / kKeys);
+            asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(kv[u].x), "r"(kv[u].y)
+                         : "memory");
+        }
         cluster_sync();
-        k = keys[to][threadIdx.x];
-        v = vals[to][threadIdx.x];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) kv[u] = pairs[to * kKeys + own + 32 * u];
     }
-    // the sorted positions and the segments
-    if (i < n) (a.passes & 1 ? a.pairs1 : a.pairs0)[i] = make_uint2(k, v);
-    const int in = (a.passes - 1) & 1;
-    if (threadIdx.x == 0) edge[0] = k;
-    if (threadIdx.x == kSortThreads - 1) edge[1] = k;
+    // the sorted pairs and the segments; here a thread takes kPer neighbours
+    const uint2* const in = pairs + ((a.passes - 1) & 1) * kKeys;
+    uint2* const out = a.passes & 1 ? a.pairs1 : a.pairs0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int i = (int)rank * kKeys + own + 32 * u;
+        if (i < n) out[i] = kv[u];
+    }
+    if (threadIdx.x == 0) {
+        edge[0] = in[0].x;
+        edge[1] = in[kKeys - 1].x;
+    }
     cluster_sync();
-    const uint32_t prev = threadIdx.x ? keys[in][threadIdx.x - 1] : rank ? remote(edge + 1, rank - 1) : rows;
-    const uint32_t next = threadIdx.x + 1 < kSortThreads ? keys[in][threadIdx.x + 1]
-                          : rank + 1 < cs ? remote(edge, rank + 1) : rows;
-    const bool valid = i < n && k < rows, begins = valid && (i == 0 || k != prev);
+    const int j0 = (int)threadIdx.x * kPer, i0 = (int)rank * kKeys + j0;
+    uint32_t key[kPer + 2];  // with the neighbours
+    key[0] = j0 ? in[j0 - 1].x : rank ? remote(edge + 1, rank - 1) : rows;
+    key[kPer + 1] = j0 + kPer < kKeys ? in[j0 + kPer].x : rank + 1 < cs ? remote(edge, rank + 1) : rows;
+    uint32_t begins = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) key[u + 1] = in[j0 + u].x;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+        if (i0 + u < n && key[u + 1] < rows && (i0 + u == 0 || key[u + 1] != key[u])) begins |= 1u << u;
     uint32_t here;
-    uint32_t seg = block_scan(begins ? 1u : 0u, warp_sum, &here) + (begins ? 1u : 0u);
+    uint32_t seg = block_scan(__popc(begins), warp_sum, &here);
     if (threadIdx.x == 0) edge[2] = here;
     cluster_sync();
     uint32_t all = 0;
@@ -514,18 +541,22 @@ k_embed_sort_small(const EmbedSort a) {
         all += c;
         if (r < rank) seg += c;
     }
-    if (valid) {
-        a.segpos[i] = seg - 1u;
-        if (begins) {
-            a.unique[seg - 1u] = k;
-            a.seg_start[seg - 1u] = (uint32_t)i;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int i = i0 + u;
+        if (i >= n || key[u + 1] >= rows) continue;
+        if ((begins >> u) & 1u) {
+            a.unique[seg] = key[u + 1];
+            a.seg_start[seg] = (uint32_t)i;
+            ++seg;
         }
-        if (i + 1 == n || next >= rows) {
+        a.segpos[i] = seg - 1u;
+        if (i + 1 == n || key[u + 2] >= rows) {
             *a.n_valid = (uint32_t)(i + 1);
             a.seg_start[all] = (uint32_t)(i + 1);
         }
     }
-    if (i == 0) {
+    if (i0 == 0) {
         *a.count = all;
         if (all == 0) *a.n_valid = a.seg_start[0] = 0u;
     }
@@ -1847,12 +1878,13 @@ void embed_sort_digits(uint64_t rows, int* passes, int* bits) {
 
 cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
     if (a.n <= kSmallSort) {
-        const int smem = kSortWarps * (1 << a.digit_bits) * 4;
-        cudaError_t e = cudaFuncSetAttribute(k_embed_sort_small,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const int per = a.n <= kSortThreads * 8 ? 1 : a.n <= kSortThreads * 16 ? 2 : 4;
+        auto f = per == 1 ? k_embed_sort_small<1> : per == 2 ? k_embed_sort_small<2> : k_embed_sort_small<4>;
+        const int smem = kSortWarps * (1 << a.digit_bits) * 4 + 2 * kSortThreads * per * 8;
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         unsigned cs = 1;
-        while (cs * kSortThreads < a.n) cs *= 2;
+        while (cs * kSortThreads * per < a.n) cs *= 2;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1867,7 +1899,7 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, k_embed_sort_small, a);
+        return cudaLaunchKernelEx(&cfg, f, a);
     }
     const int blocks = embed_sort_blocks(a.n);
     const int smem = kSortWarps * (1 << a.digit_bits) * 4 + kSortThreads * kSortBatch * 8;

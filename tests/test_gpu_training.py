@@ -121,7 +121,10 @@ def ids_like(kind, n, rows, seed):
 SPARSE = [("zipf", 1, 7, 8, 1), ("zipf", 33, 300, 64, 2), ("one", 700, 10, 264, 1),
           ("distinct", 500, 600, 32, 1), ("masked", 65, 10, 64, 1), ("zipf", 5000, 129_280, 40, 3),
           ("zipf", 30_000, 64_000_000, 32, 1), ("one", 20_001, 4_000_000_000, 8, 1),
-          ("zipf", 2000, 511, 5120, 4), ("zipf", 2000, 512, 256, 1), ("zipf", 8193, 1, 16, 1)]
+          ("zipf", 8192, 5000, 16, 1), ("zipf", 16_384, 70_000, 8, 1), ("zipf", 16_385, 9, 8, 1),
+          ("distinct", 32_768, 32_768, 8, 1), ("zipf", 32_769, 800_000, 8, 1),
+          ("zipf", 1_300_000, 40_000_000, 8, 1), ("one", 160_000, 5, 8, 2),
+          ("masked", 40_000, 5, 8, 1), ("zipf", 2000, 511, 5120, 4), ("zipf", 2000, 512, 256, 1), ("zipf", 8193, 1, 16, 1)]
 
 
 @pytest.mark.parametrize("kind,n,rows,dim,copies", SPARSE)
