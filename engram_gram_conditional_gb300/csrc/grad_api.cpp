@@ -235,9 +235,11 @@ LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim, bo
     const int64_t piece = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
     const GradProblem dx = loss_dx(T, dim, piece), dh = loss_dhead(T, dim, piece, piece);
     LossBackWs w{};
+    // the splits' fp32 dx stay within 64 MB, as dz does
+    const int fit = (int)std::max<int64_t>(1, ((int64_t)64 << 20) / (T * (int64_t)dim * 4));
     // with and without the other product the cut may differ: room for either
-    w.splits = long_splits(dx, want_dhead ? &dh : nullptr);
-    const int most = std::max(w.splits, long_splits(dx, want_dhead ? nullptr : &dh));
+    w.splits = std::min(fit, long_splits(dx, want_dhead ? &dh : nullptr));
+    const int most = std::max(w.splits, std::min(fit, long_splits(dx, want_dhead ? nullptr : &dh)));
     Carver c(p);
     w.dz = c.take<uint16_t>((size_t)rows * piece);
     w.acc = c.take<float>(most > 1 || piece < vocab ? (size_t)most * T * dim : 0);

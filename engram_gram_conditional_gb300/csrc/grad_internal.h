@@ -1,5 +1,6 @@
 // Internal declarations of the training operators: their kernels' launchers
-// (kernels_grad.cu, kernels_train.cu) as grad_api.cpp calls them.
+// (kernels_grad.cu, kernels_few.cu, kernels_embed.cu, kernels_gate.cu) as
+// grad_api.cpp calls them.
 #pragma once
 
 #include "engram_internal.h"
@@ -93,7 +94,7 @@ cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, const flo
                               uint16_t* out, cudaStream_t s);
 
 
-// ---- embedding (kernels_train.cu) ----
+// ---- embedding (kernels_embed.cu) ----
 cudaError_t launch_embed(const void* table, bool f32, uint64_t rows, int dim, const uint32_t* ids,
                          int64_t n, float scale, int copies, uint16_t* out, uint32_t* err,
                          cudaStream_t s);
@@ -135,7 +136,7 @@ struct EmbedSum {
 int embed_rows_per_chunk(int64_t n, int dim, int copies);
 cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s);
 
-// ---- gate (kernels_train.cu) ----
+// ---- gate (kernels_gate.cu) ----
 enum SavedKind : int { kSavedF32 = 0, kSavedBf16 = 1, kSavedMx = 2 };  // as ENGRAM_KV_*
 struct GateTrain {
     int64_t T;

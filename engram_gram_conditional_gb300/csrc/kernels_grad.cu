@@ -53,7 +53,7 @@ constexpr int kBox = 32 * 64 * 2;
 // Shared memory of each variant.
 template <int kEpi>
 struct Layout {
-    static constexpr int kStages = kEpi == kGradLse ? 7 : 6;
+    static constexpr int kStages = 6;
     static constexpr int kOffOut = kStages * kStage;
     static constexpr int kOffBar = kOffOut + (kEpi == kGradLse ? 0 : kEpiWarps * kBox);
     static constexpr int kNumBars = 2 * kStages + 4;
@@ -240,7 +240,8 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
 
     if (warp == kWarpTma) {
         if (lane == 0) {
-            int it = 0;
+            int s = 0;
+            uint32_t phase = 1;  // of the stage's empty barrier
             bool ok = !a.starve;
             for (int i = 0; i < n_items && ok; ++i) {
                 const Item w = get_item(a, pair, pairs, n_long, i);
@@ -249,10 +250,9 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                 const CUtensorMap* tmB = w.pr ? &tmB1 : &tmB0;
                 const int mb = 2 * w.mu + (int)rank;               // this CTA's 128 rows of A
                 const int n0 = w.nt * kBN + (int)rank * (kBN / 2);  // and its half of B
-                for (int j = 0; j < w.nkb; ++j, ++it) {
-                    const int s = it % kStages;
+                for (int j = 0; j < w.nkb; ++j) {
                     const int kb = w.kb_lo + j;
-                    if (!mbar_wait(empty(s), ((uint32_t)(it / kStages) & 1u) ^ 1u, abort_flag, lim)) {
+                    if (!mbar_wait(empty(s), phase, abort_flag, lim)) {
                         fail();
                         ok = false;
                         break;
@@ -280,12 +280,17 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                     } else {
                         tma_load_2d_pair(sb, tmB, bar, kb * kBK, n0);
                     }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
         }
     } else if (warp == kWarpMma) {
         if (lane == 0 && issuer) {
-            int it = 0, use = 0;  // stages, accumulators used so far
+            int s = 0, use = 0;  // stage, accumulators used so far
+            uint32_t phase = 0;  // of the stage's full barrier
             bool ok = true;
             for (int i = 0; i < n_items && ok; ++i) {
                 const GradProblem& q = a.pr[i < n_long ? 0 : 1];
@@ -294,39 +299,37 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                 const uint32_t id = grad_idesc(a_mn, kBMn);
                 // 16 of the reduction: 32 bytes of a K-major row, or 16 rows of 128 bytes
                 const uint64_t a_step = a_mn ? 128ull : 2ull, b_step = kBMn ? 128ull : 2ull;
-                uint32_t d_tmem = 0;
-                int seg = 0;  // k-blocks in the current accumulator
-                for (int j = 0; j < nkb; ++j, ++it) {
-                    const int s = it % kStages;
-                    if (seg == 0) {
-                        const int acc = use & 1;
-                        if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(use >> 1) & 1u) ^ 1u, abort_flag, lim)) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        d_tmem = tmem_base + (uint32_t)(acc * kBN);
-                    }
-                    if (!mbar_wait_cluster(full(s), (uint32_t)(it / kStages) & 1u, abort_flag, lim)) {
+                const uint64_t a_desc = a_mn ? sdesc_mn(sbase) : sdesc_sw128(sbase);
+                const uint64_t b_desc = kBMn ? sdesc_mn(sbase + kOperand) : sdesc_sw128(sbase + kOperand);
+                for (int kb0 = 0; kb0 < nkb && ok; kb0 += kSegment, ++use) {
+                    const int acc = use & 1, n = min(kSegment, nkb - kb0);
+                    if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(use >> 1) & 1u) ^ 1u, abort_flag, lim)) {
                         fail();
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = sbase + (uint32_t)(s * kStage), sb = sa + kOperand;
-                    const uint64_t ad = a_mn ? sdesc_mn(sa) : sdesc_sw128(sa);
-                    const uint64_t bd = kBMn ? sdesc_mn(sb) : sdesc_sw128(sb);
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
+                    for (int j = 0; j < n; ++j) {
+                        if (!mbar_wait_cluster(full(s), phase, abort_flag, lim)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        // (a stage is kStage / 16 descriptor units further)
+                        const uint64_t ad = a_desc + (uint64_t)(s * (kStage >> 4));
+                        const uint64_t bd = b_desc + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        umma_f16kind_pair(d_tmem, ad + a_step * k, bd + b_step * k, id,
-                                          (seg != 0) || (k != 0));
-                    umma_commit_pair(empty(s));
-                    if (++seg == kSegment || j + 1 == nkb) {
-                        umma_commit_pair(tfull(use & 1));
-                        ++use;
-                        seg = 0;
+                        for (int k = 0; k < kBK / 16; ++k)
+                            umma_f16kind_pair(d_tmem, ad + a_step * k, bd + b_step * k, id, (j != 0) || (k != 0));
+                        umma_commit_pair(empty(s));
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
+                    if (ok) umma_commit_pair(tfull(acc));
                 }
             }
         }
