@@ -461,7 +461,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
         if (e == cudaSuccess) e = make_tma_16bit(&tm[3], d_emb, T, K, 64, false);
     }
     if (d_demb && e == cudaSuccess) {
-        a.pr[0] = product(T, K, N, false);
+        a.pr[0] = product(T, ctx->K, ctx->N, false);
         a.pr[0].out = d_demb;
         a.pr[0].splits = long_splits(a.pr[0], d_dwkv ? &a.pr[1] : nullptr);
         if (a.pr[0].splits > 1) {

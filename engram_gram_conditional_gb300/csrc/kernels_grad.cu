@@ -29,6 +29,7 @@
 // pair).  Every wait is bounded as in kernels_mma.cu.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "grad_internal.h"
@@ -158,6 +159,13 @@ __device__ __forceinline__ int item_count(const GradArgs& a, int p, int pairs) {
     return nh + (upto > b ? (upto - b + fewer - 1) / fewer : 0) + all;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+
 // n / d for n < 2^31 (see fast_div on the host).
 __device__ __forceinline__ int divide(int n, const FastDiv& d) {
     return d.d == 1 ? n : (int)(__umulhi((uint32_t)n, d.m) >> d.s);
@@ -193,8 +201,8 @@ __device__ __forceinline__ Item get_item(const GradArgs& a, int p, int pairs, in
     return it;
 }
 
-// kEpi: what becomes of a tile.  kBMn: B is MN-major (the gradient products).
-template <int kEpi, bool kBMn>
+// kEpi: what becomes of a tile.
+template <int kEpi>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
@@ -247,83 +255,112 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
     };
 
     if (warp == kWarpTma) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t phase = 1;  // of the stage's empty barrier
-            bool ok = !a.starve;
-            for (int i = 0; i < n_items && ok; ++i) {
-                const Item w = get_item(a, pair, pairs, n_long, i);
-                const GradProblem& q = a.pr[w.pr];
-                const CUtensorMap* tmA = w.pr ? &tmA1 : &tmA0;
-                const CUtensorMap* tmB = w.pr ? &tmB1 : &tmB0;
-                const int mb = 2 * w.mu + (int)rank;               // this CTA's 128 rows of A
-                const int n0 = w.nt * kBN + (int)rank * (kBN / 2);  // and its half of B
-                for (int j = 0; j < w.nkb; ++j) {
-                    const int kb = w.kb_lo + j;
-                    if (!mbar_wait(empty(s), phase, abort_flag, lim)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    if (issuer) mbar_expect_tx(full(s), 2 * kStage);
-                    const uint32_t bar = map_rank(full(s), 0);
+        // The whole warp walks the items, one elected lane loads: coordinates and
+        // addresses stay in uniform registers, and what does not change within an
+        // item is out of the loop.  (The tensor cores feel every few instructions
+        // in the load and issue loops, 1-5% of a launch; the issuing warp is best
+        // walked by one lane alone.)
+        const bool leader = elect_one();
+        auto wait = [&](uint32_t b, uint32_t parity) {
+            bool ok = true;
+            if (kEpi == kGradOut) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_suspended(b, parity, abort_flag, lim));
+            } else {  // (one lane waits: 2% less for the softmax epilogues, 1% more for the products)
+                if (lane == 0) ok = mbar_wait_suspended(b, parity, abort_flag, lim);
+                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            }
+            if (!ok && leader) fail();
+            return ok;
+        };
+        int s = 0;
+        uint32_t phase = 1;  // of the stage's empty barrier
+        const uint32_t full0 = map_rank(full(0), 0);  // the even CTA's barriers
+        bool ok = !a.starve;
+        for (int i = 0; i < n_items && ok; ++i) {
+            const Item w = get_item(a, pair, pairs, n_long, i);
+            const GradProblem& q = a.pr[w.pr];
+            const CUtensorMap* tmA = w.pr ? &tmA1 : &tmA0;
+            const CUtensorMap* tmB = w.pr ? &tmB1 : &tmB0;
+            const int mb = 2 * w.mu + (int)rank;               // this CTA's 128 rows of A
+            const int n0 = w.nt * kBN + (int)rank * (kBN / 2);      // and its half of B
+            // the A box of the first k-block, its steps to the next (from an even and
+            // from an odd block), and an MN-major operand's second box
+            constexpr bool b_mn = kEpi == kGradOut;  // (the products read B as it lies)
+            const bool a_mn = kEpi == kGradOut && q.a_mn;
+            const int tiled = kEpi == kGradOut ? q.a_tiled : 0;
+            int ax, ay, asx = 0, as0, as1, aox = 0, aoy = 0;
+            if (a_mn && tiled) {  // 128 x 64 tiles [reduction block][M chunk]
+                ax = 0;
+                ay = ((w.kb_lo >> 1) * tiled + 2 * mb) * 128 + (w.kb_lo & 1) * 64;
+                as0 = 64;
+                as1 = tiled * 128 - 64;
+                aoy = 128;
+            } else if (a_mn) {
+                ax = mb * kBM;
+                ay = w.kb_lo * kBK;
+                as0 = as1 = kBK;
+                aox = 64;
+            } else if (tiled) {  // 128 x 64 tiles [M block][reduction chunk]
+                ax = 0;
+                ay = (mb * tiled + w.kb_lo) * 128;
+                as0 = as1 = 128;
+            } else {
+                ax = w.kb_lo * kBK;
+                ay = mb * kBM;
+                asx = kBK;
+                as0 = as1 = 0;
+            }
+            int bx = b_mn ? n0 : w.kb_lo * kBK, by = b_mn ? w.kb_lo * kBK : n0;
+            const int bsx = b_mn ? 0 : kBK, bsy = b_mn ? kBK : 0;
+            bool odd = (w.kb_lo & 1) != 0;
+            for (int j = 0; j < w.nkb; ++j) {
+                ok = wait(empty(s), phase);
+                if (!ok) break;
+                if (leader) {
                     const uint32_t sa = sbase + (uint32_t)(s * kStage), sb = sa + kOperand;
-                    if (q.a_mn) {
-                        if (q.a_tiled) {  // 128 x 64 tiles [reduction block][M chunk]
-                            const int y = ((kb >> 1) * q.a_tiled + 2 * mb) * 128 + (kb & 1) * 64;
-                            tma_load_2d_pair(sa, tmA, bar, 0, y);
-                            tma_load_2d_pair(sa + kChunk, tmA, bar, 0, y + 128);
-                        } else {
-                            tma_load_2d_pair(sa, tmA, bar, mb * kBM, kb * kBK);
-                            tma_load_2d_pair(sa + kChunk, tmA, bar, mb * kBM + 64, kb * kBK);
-                        }
-                    } else if (q.a_tiled) {  // 128 x 64 tiles [M block][reduction chunk]
-                        tma_load_2d_pair(sa, tmA, bar, 0, (mb * q.a_tiled + kb) * 128);
-                    } else {
-                        tma_load_2d_pair(sa, tmA, bar, kb * kBK, mb * kBM);
-                    }
-                    if (kBMn) {
-                        tma_load_2d_pair(sb, tmB, bar, n0, kb * kBK);
-                        tma_load_2d_pair(sb + kChunk, tmB, bar, n0 + 64, kb * kBK);
-                    } else {
-                        tma_load_2d_pair(sb, tmB, bar, kb * kBK, n0);
-                    }
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                    const uint32_t bar = full0 + 8u * (uint32_t)s;
+                    if (issuer) mbar_expect_tx(full(s), 2 * kStage);
+                    tma_load_2d_pair(sa, tmA, bar, ax, ay);
+                    if (a_mn) tma_load_2d_pair(sa + kChunk, tmA, bar, ax + aox, ay + aoy);
+                    tma_load_2d_pair(sb, tmB, bar, bx, by);
+                    if (b_mn) tma_load_2d_pair(sb + kChunk, tmB, bar, bx + 64, by);
+                }
+                ax += asx;
+                ay += odd ? as1 : as0;
+                odd = !odd;
+                bx += bsx;
+                by += bsy;
+                if (++s == kStages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0 && issuer) {
+        if (issuer && lane == 0) {
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                const bool ok = mbar_wait_suspended(b, parity, abort_flag, lim);
+                if (!ok) fail();
+                return ok;
+            };
             int s = 0, use = 0;  // stage, accumulators used so far
             uint32_t phase = 0;  // of the stage's full barrier
-            bool ok = true;
-            for (int i = 0; i < n_items && ok; ++i) {
-                const GradProblem& q = a.pr[i < n_long ? 0 : 1];
-                const int nkb = q.splits > 1 ? get_item(a, pair, pairs, n_long, i).nkb : q.kb;
-                const bool a_mn = q.a_mn != 0;
-                const uint32_t id = grad_idesc(a_mn, kBMn);
+            // nkb k-blocks of operands stored as kAMn and kBMn say, kSegment to an
+            // accumulator; false on a time-out
+            auto issue = [&](auto kAMn, auto kBMn, int nkb) {
+                constexpr bool a_mn = decltype(kAMn)::value, b_mn = decltype(kBMn)::value;
+                constexpr uint32_t id = grad_idesc(a_mn, b_mn);
                 // 16 of the reduction: 32 bytes of a K-major row, or 16 rows of 128 bytes
-                const uint64_t a_step = a_mn ? 128ull : 2ull, b_step = kBMn ? 128ull : 2ull;
+                constexpr uint64_t a_step = a_mn ? 128ull : 2ull, b_step = b_mn ? 128ull : 2ull;
                 const uint64_t a_desc = a_mn ? sdesc_mn(sbase) : sdesc_sw128(sbase);
-                const uint64_t b_desc = kBMn ? sdesc_mn(sbase + kOperand) : sdesc_sw128(sbase + kOperand);
-                for (int kb0 = 0; kb0 < nkb && ok; kb0 += kSegment, ++use) {
+                const uint64_t b_desc = b_mn ? sdesc_mn(sbase + kOperand) : sdesc_sw128(sbase + kOperand);
+                for (int kb0 = 0; kb0 < nkb; kb0 += kSegment, ++use) {
                     const int acc = use & 1, n = min(kSegment, nkb - kb0);
-                    if (!mbar_wait_cluster(tempty(acc), ((uint32_t)(use >> 1) & 1u) ^ 1u, abort_flag, lim)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
+                    if (!wait(tempty(acc), ((uint32_t)(use >> 1) & 1u) ^ 1u)) return false;
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
                     for (int j = 0; j < n; ++j) {
-                        if (!mbar_wait_cluster(full(s), phase, abort_flag, lim)) {
-                            fail();
-                            ok = false;
-                            break;
-                        }
+                        if (!wait(full(s), phase)) return false;
                         tc_fence_after();
                         // (a stage is kStage / 16 descriptor units further)
                         const uint64_t ad = a_desc + (uint64_t)(s * (kStage >> 4));
@@ -337,8 +374,23 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
                             phase ^= 1u;
                         }
                     }
-                    if (ok) umma_commit_pair(tfull(acc));
+                    umma_commit_pair(tfull(acc));
                 }
+                return true;
+            };
+            using Mn = std::true_type;
+            using K = std::false_type;
+            bool ok = true;
+            for (int i = 0; i < n_items && ok; ++i) {
+                const GradProblem& q = a.pr[i < n_long ? 0 : 1];
+                int nkb = q.kb;
+                if (q.splits > 1) nkb = get_item(a, pair, pairs, n_long, i).nkb;
+                if constexpr (kEpi != kGradOut)
+                    ok = issue(K{}, K{}, nkb);
+                else if (q.a_mn)
+                    ok = issue(Mn{}, Mn{}, nkb);
+                else
+                    ok = issue(K{}, Mn{}, nkb);
             }
         }
     } else {
@@ -352,7 +404,7 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
         auto acc_ready = [&]() {
             const int acc = use & 1;
             int ready = 1;
-            if (lane == 0) ready = mbar_wait_cluster(tfull(acc), (uint32_t)(use >> 1) & 1u, abort_flag, lim);
+            if (lane == 0) ready = mbar_wait_suspended(tfull(acc), (uint32_t)(use >> 1) & 1u, abort_flag, lim);
             ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
             if (!ready && lane == 0) fail();
             tc_fence_after();
@@ -676,11 +728,11 @@ cudaError_t pdl_launch(void* f, dim3 grid, dim3 block, void** args, cudaStream_t
 
 // CTA pairs that are resident at once: a launch has no more, since its items are
 // dealt out for pairs that all run from the start.
-template <int kEpi, bool kBMn>
+template <int kEpi>
 cudaError_t resident_pairs(int* pairs) {
     static int known = 0;
     if (!known) {
-        auto kern = k_grad<kEpi, kBMn>;
+        auto kern = k_grad<kEpi>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Layout<kEpi>::kSmem);
         if (e != cudaSuccess) return e;
@@ -705,9 +757,9 @@ cudaError_t resident_pairs(int* pairs) {
     return cudaSuccess;
 }
 
-template <int kEpi, bool kBMn>
+template <int kEpi>
 cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
-    auto kern = k_grad<kEpi, kBMn>;
+    auto kern = k_grad<kEpi>;
     for (GradProblem& q : a.pr) {
         q.items = q.m_units * q.n_tiles * q.splits;
         if (!q.items) continue;
@@ -719,7 +771,7 @@ cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
     const int total = a.pr[0].items + a.pr[1].items;
     if (!total) return cudaSuccess;
     int pairs = 0;
-    cudaError_t e = resident_pairs<kEpi, kBMn>(&pairs);
+    cudaError_t e = resident_pairs<kEpi>(&pairs);
     if (e != cudaSuccess) return e;
     pairs = std::min(pairs, total);
     share_items(a, pairs);
@@ -741,13 +793,13 @@ cudaError_t launch(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
 int grad_pairs() { return device_sm_count() / 2; }
 
 cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
-    return launch<kGradLse, false>(a, tm, s);
+    return launch<kGradLse>(a, tm, s);
 }
 cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
-    return launch<kGradDz, false>(a, tm, s);
+    return launch<kGradDz>(a, tm, s);
 }
 cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s) {
-    return launch<kGradOut, true>(a, tm, s);
+    return launch<kGradOut>(a, tm, s);
 }
 
 cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,

@@ -44,6 +44,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         }
     }
 }
+// The same bounded wait for kernels whose waits are long: the thread is suspended
+// for up to a millisecond at a time instead of polling, which at the power limit
+// leaves watts to the tensor cores (kernels_grad.cu: 2-6% of a launch).  Waking up
+// takes longer: kernels bound by memory lost 1-3% with it and poll.
+__device__ __forceinline__ bool mbar_try_wait_suspended(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                    long long limit_ns) {
+    if (mbar_try_wait_suspended(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+        if (mbar_try_wait_suspended(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if ((long long)(globaltimer() - t0) > limit_ns) return false;
+    }
+}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -434,7 +434,9 @@ def test_gate_backward_at_a_dot_of_zero(where):
 @pytest.mark.parametrize("want", ["both", "demb", "dwkv"])
 @pytest.mark.parametrize("T,hc,d,heads,row_dim", [(1, 1, 256, 2, 32), (63, 1, 256, 2, 32),
                                                   (64, 2, 256, 1, 64), (130, 1, 512, 3, 128),
-                                                  (257, 3, 256, 8, 64), (700, 1, 256, 5, 256)])
+                                                  (257, 3, 256, 8, 64), (700, 1, 256, 5, 256),
+                                                  (333, 2, 512, 4, 128), (1037, 1, 256, 2, 64),
+                                                  (20, 4, 1280, 2, 128)])
 def test_project_backward(T, hc, d, heads, row_dim, want):
     N, K = (hc + 1) * d, 3 * heads * row_dim
     wkv, emb, dkv = rnd(1, N, K), rnd(T, T, K), rnd(T + 1, T, N)
