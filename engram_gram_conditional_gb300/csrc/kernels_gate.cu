@@ -6,9 +6,10 @@
 // outputs, and both are bound by memory if the second reading is not from HBM.
 // So a cluster of CTAs keeps a token in shared memory between the two.  At hc 4,
 // d 5,120 and 2,048 tokens (GB300, copy bandwidth 6.77 TB/s): forward with fp32
-// kv 87 us (475 MB, 81%; a block per token that reads hidden again 97); backward
-// from the checkpoint 82 us (370 MB, 67%: the kernel 76, bound by HBM and by its
-// issue rate, and the weights' sums 6; two kernels over the tokens 214).
+// kv 86 us (475 MB, 81%; a block per token that reads hidden again 97), with BF16
+// kv 76; backward from the checkpoint 81 us (370 MB, 67%: the kernel 75, bound by
+// HBM and by its issue rate, and the weights' sums 6; two kernels over the tokens
+// 214), from BF16 kv 89, from fp32 kv 111.
 #include <algorithm>
 
 #include "grad_internal.h"
@@ -160,7 +161,7 @@ __device__ __forceinline__ float4 gate_factors(float skk, float shh, float s, fl
 // values (f32x2), and an 8-bit block's scale multiplies the sums and factors
 // instead of its values.
 constexpr int kFusedMaxWarps = 10;  // compute warps
-constexpr int kFusedSlots = 4;      // tokens between phase 1 and phase 2 at most 2
+constexpr int kFusedSlots = 4;      // exchanges: those of the tokens in flight and one more
 constexpr int kFusedMaxStages = 8;
 constexpr int kFusedFixed =
     kFusedSlots * (kFusedMaxWarps * 32 + 8 * 32 + 32) * 4 + (2 * kFusedMaxStages + 3 * kFusedSlots) * 8 + 128;
@@ -221,7 +222,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN], int lane) {
 // kExact: hc == kHc (no branch is left out).
 template <int kSaved, int kHc, bool kExact>
 __global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
-k_gate_backward_fused(const GateTrain a, int stages, int cs) {
+k_gate_backward_fused(const GateTrain a, int stages, int cs, int lag) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSums = 4 * kHc;
     const int hc = kExact ? kHc : a.hc;
@@ -397,8 +398,9 @@ k_gate_backward_fused(const GateTrain a, int stages, int cs) {
             return *reinterpret_cast<const uint4*>(
                 st + (fused_row_bytes<kSaved>(hc) - 2 * hc + 2 * b) * max_cols + 2 * lc);
         };
-        for (int i = 0; i <= n; ++i) {
-            const bool image = i > 0 && a.windows[token(i - 1)].x == kDead;  // of phase 2's token
+        for (int i = 0; i < n + lag; ++i) {
+            const int p = i - lag;  // phase 2's token
+            const bool image = p >= 0 && a.windows[token(p)].x == kDead;
             if (i < n) {
                 const int s = i % stages;
                 const uint8_t* st = ring + s * stage_bytes;
@@ -440,8 +442,8 @@ k_gate_backward_fused(const GateTrain a, int stages, int cs) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(parts(i));
             }
-            if (i == 0) continue;
-            const int p = i - 1, s = p % stages;
+            if (p < 0) continue;
+            const int s = p % stages;
             const uint8_t* st = ring + s * stage_bytes;
             const int64_t t = token(p);
             if (!wait(factors(p), slot_phase(p))) break;
@@ -525,7 +527,7 @@ __device__ __forceinline__ uint2 encode_mx8(const f32x2 (&v)[4], uint32_t& expon
 
 template <bool kF32Kv, int kHc, bool kExact>
 __global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
-k_gate_checkpoint_fused(const GateTrain a, int stages, int cs) {
+k_gate_checkpoint_fused(const GateTrain a, int stages, int cs, int lag) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSums = 4 * kHc;  // (three used per branch)
     const int hc = kExact ? kHc : a.hc;
@@ -661,12 +663,13 @@ k_gate_checkpoint_fused(const GateTrain a, int stages, int cs) {
                 unpack8(*reinterpret_cast<const uint4*>(st + 2 * ((hc + r) * max_cols + lc)), f);
             }
         };
-        uint32_t id = n > 0 ? a.windows[token(0)].x : 0u, id_before = 0u;
-        for (int i = 0; i <= n; ++i) {
-            // slot 0 of the windows of the tokens in phases 1 and 2, the next one's on its way
-            const bool img = id == kDead, image = id_before == kDead;
-            id_before = id;
+        uint32_t id = n > 0 ? a.windows[token(0)].x : 0u;
+        for (int i = 0; i < n + lag; ++i) {
+            const int p = i - lag;  // phase 2's token
+            // (slot 0 of the windows of the tokens in both phases, on their way early)
+            const bool img = id == kDead;
             if (i + 1 < n) id = a.windows[token(i + 1)].x;
+            const bool image = p >= 0 && a.windows[token(p)].x == kDead;
             if (i < n) {
                 const int64_t t = token(i);
                 const int s = i % stages;
@@ -713,8 +716,8 @@ k_gate_checkpoint_fused(const GateTrain a, int stages, int cs) {
                 keyvalue(st, hc, v);
                 keep(2 * hc, v);
             }
-            if (i == 0) continue;
-            const int p = i - 1, s = p % stages;
+            if (p < 0) continue;
+            const int s = p % stages;
             const uint8_t* st = ring + s * stage_bytes;
             uint16_t* ho = a.hidden_out + token(p) * (int64_t)hc * d + col0 + lc;
             if (!wait(gates_in(p), slot_phase(p))) break;
@@ -959,15 +962,18 @@ k_gate_backward_weights(const GateTrain a, int shares) {
 }
 
 // Cluster size and stages of a one-pass kernel for d columns and a stage of
-// bytes(cols) bytes; 0 if no cluster holds three stages of a token (one in each
-// phase and one on its way).
+// bytes(cols) bytes; 0 if no cluster holds two.  The smallest cluster that does:
+// at hc 4, d 5,120 two CTAs with two stages of fp32 kv and gradient (and no lag)
+// 111 us, four with four stages 144, since half as many warps share an SM's
+// work.  The lag is what the stages allow beside one that fills: none of two, one
+// of three, two of four or more.
 template <class Bytes>
 int one_pass_cluster(int d, Bytes bytes, int* stages) {
     const int groups = d / 256;
     for (int cs = 1; cs <= 8 && cs <= groups; cs *= 2) {
         const int per = (groups + cs - 1) / cs;
         const int n = (227 * 1024 - kFusedFixed - 128) / bytes(per * 256);
-        if (per <= kFusedMaxWarps && n >= 3) {
+        if (per <= kFusedMaxWarps && n >= 2) {
             *stages = std::min(n, 6);
             return cs;
         }
@@ -990,14 +996,20 @@ cudaError_t one_pass_launch(F kern, const GateTrain& a, int cs, int stages, int 
     attr[1].val.clusterDim.x = cs;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    *clusters = (int)std::min<int64_t>(a.T, device_sm_count() / cs);
-    cfg.gridDim = dim3(*clusters * cs);
+    // (as many clusters as are resident at once: larger ones leave SMs of a GPC over)
+    int resident = device_sm_count();
+    cfg.gridDim = dim3(device_sm_count() / cs * cs);
     cfg.blockDim = dim3((per + 2) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (cs > 1 && (e = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg)) != cudaSuccess) return e;
+    *clusters = (int)std::min<int64_t>(a.T, std::max(1, std::min(resident, device_sm_count() / cs)));
+    cfg.gridDim = dim3(*clusters * cs);
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs);
+    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs, std::min(2, stages - 2));
 }
 
 template <int kSaved, int kHc>

@@ -17,10 +17,10 @@
 // short one (dhead, dwkv) fills the pairs up, so that they end together.
 //
 // Bound by the tensor cores, and these by the power limit: over seconds cuBLAS
-// BF16 runs at 1,722 TFLOP/s on the same GPU (1,920 in bursts).  2,048 tokens,
-// 129,280 x 5,120: loss 1.65 ms (1,650 TFLOP/s), its backward pass 4.97 ms
-// (1,640); project backward at 25,600 x 6,144 0.78 ms (1,650).  In one short
-// launch the tensor pipe is active 80-83% of the cycles.  256 x 256 tiles on
+// BF16 runs at 1,722 TFLOP/s on such a GPU (1,920 in bursts).  2,048 tokens,
+// 129,280 x 5,120, back to back: loss 1.53 ms (1,770 TFLOP/s), its backward pass
+// 4.70 ms (1,730); project backward at 25,600 x 6,144 0.73 ms (1,770).  In one
+// short launch the tensor pipe is active 80-83% of the cycles.  256 x 256 tiles on
 // pairs: a pair takes in 64 KB per 512 cycles of MMA, two thirds of what two
 // single CTAs with 128 x 256 tiles would.  Six stages: five or seven differ by 1-2%.
 //
