@@ -248,7 +248,7 @@ def gate_ref(h, kv, on, wq, wk, eps=1e-6):
     return h + gate * v, gate, dot
 
 
-GATE = [(1, 1, 256), (3, 2, 512), (5, 4, 1024), (7, 3, 768), (2, 8, 256), (9, 5, 2816)]
+GATE = [(1, 1, 256), (3, 2, 512), (5, 4, 1024), (7, 3, 512), (2, 8, 256), (9, 5, 2816)]
 
 
 @pytest.mark.parametrize("kv_format", [eg.KV_F32, eg.KV_BF16])
