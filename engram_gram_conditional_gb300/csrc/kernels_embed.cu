@@ -62,12 +62,12 @@ constexpr int kSortBatch = 8;  // rounds of 32 keys that a warp loads at once
 constexpr int kSmallSort = kSortThreads * 8 * 4;  // keys of the one-cluster sort
 
 // A barrier of the cooperative launch's blocks in two halves, so that a block can
-// work between them; the wait is bounded: false on a time-out.
+// work between them; the wait is bounded: false on a time-out.  The block's barrier
+// orders its writes before the release, and the acquire before what it reads next.
 __device__ __forceinline__ void grid_arrive(const EmbedSort& a) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(a.barrier, 1u);
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.barrier) : "memory");
     }
 }
 __device__ __forceinline__ bool grid_wait(const EmbedSort& a, uint32_t& phase, int* flag) {
@@ -82,7 +82,6 @@ __device__ __forceinline__ bool grid_wait(const EmbedSort& a, uint32_t& phase, i
                 break;
             }
         }
-        __threadfence();
     }
     __syncthreads();
     return *flag == 0;
@@ -673,9 +672,12 @@ k_embed_sum(const EmbedSum a) {
 
 // The rows of the segments that left partial sums: the tail of the chunk in which
 // one begins and the heads of the chunks after it, added in order.  A block looks
-// for them in `look` chunks (at most kJoinMost), then each warp takes one after the other; one
-// of more than kJoinAlone parts (a hot id) is added by the whole block, each warp
-// a contiguous share, then the shares in order.
+// for them in `look` chunks (at most kJoinMost), then each group of `lanes` threads
+// takes one after the other; one of more than kJoinAlone parts (a hot id) is added
+// by the whole block, each group a contiguous share, then the shares in order.
+// (3 million rows of 8 columns, 200,000 ids: 484 us with whole warps as groups,
+// 397 so.  Looking for the segments before the sums have ended takes blocks from
+// them: 275 us against 271 at 50,032 x 24 rows of 256.)
 constexpr int kJoinMost = 64, kJoinAlone = 32;
 
 __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int64_t p0, int64_t p1, int col,
@@ -693,11 +695,11 @@ __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int6
 __global__ void __launch_bounds__(256, 3)
 k_embed_join(const EmbedSum a, int64_t chunks, int look) {
     pdl_wait();
-    __shared__ float sm[8][32][9];
+    __shared__ float sm[256][9];
     __shared__ int parts_of[kJoinMost];
     __shared__ uint32_t seg_of[kJoinMost];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = ((int)blockIdx.y * 32 + lane) * 8;
+    const int groups = 256 / a.lanes, g = threadIdx.x / a.lanes;
+    const int col = ((int)blockIdx.y * a.lanes + (int)threadIdx.x % a.lanes) * 8;
     const int64_t first = (int64_t)blockIdx.x * look;
     if ((int)threadIdx.x < look) {
         const int64_t nv = *a.n_valid;
@@ -720,7 +722,7 @@ k_embed_join(const EmbedSum a, int64_t chunks, int look) {
         seg_of[threadIdx.x] = seg;
     }
     __syncthreads();
-    for (int c = warp; c < look; c += 8) {
+    for (int c = g; c < look; c += groups) {
         const int parts = parts_of[c];
         if (parts == 0 || parts > kJoinAlone || col >= a.dim) continue;
         float acc[8] = {};
@@ -731,14 +733,14 @@ k_embed_join(const EmbedSum a, int64_t chunks, int look) {
         const int64_t parts = parts_of[c];
         if (parts <= kJoinAlone) continue;
         float acc[8] = {};
-        add_parts(a, first + c, parts * warp / 8, parts * (warp + 1) / 8, col, acc);
+        add_parts(a, first + c, parts * g / groups, parts * (g + 1) / groups, col, acc);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sm[warp][lane][j] = acc[j];
+        for (int j = 0; j < 8; ++j) sm[threadIdx.x][j] = acc[j];
         __syncthreads();
-        if (warp == 0 && col < a.dim) {
-            for (int x = 1; x < 8; ++x)
+        if (g == 0 && col < a.dim) {
+            for (int x = 1; x < groups; ++x)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] += sm[x][lane][j];
+                for (int j = 0; j < 8; ++j) acc[j] += sm[x * a.lanes + threadIdx.x][j];
             put_row(a, seg_of[c], col, acc);
         }
         __syncthreads();
@@ -832,7 +834,7 @@ cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
     cudaError_t e = pdl_launch(f, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
     if (e != cudaSuccess || chunks < 2) return e;
     // about four blocks per SM
-    const int64_t slices = (a.dim + 255) / 256, want = chunks * slices / (device_sm_count() * 4) + 1;
+    const int64_t slices = a.slices, want = chunks * slices / (device_sm_count() * 4) + 1;
     const int look = (int)std::min<int64_t>(kJoinMost, std::max<int64_t>(8, want));
     return pdl_launch(k_embed_join, dim3((unsigned)((chunks + look - 1) / look), (unsigned)slices), dim3(256), 0, s,
                       a, chunks, look);
