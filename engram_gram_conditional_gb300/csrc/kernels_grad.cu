@@ -18,8 +18,8 @@
 //
 // Bound by the tensor cores, and these by the power limit: over seconds cuBLAS
 // BF16 runs at 1,722 TFLOP/s on such a GPU (1,920 in bursts).  2,048 tokens,
-// 129,280 x 5,120, back to back: loss 1.53 ms (1,770 TFLOP/s), its backward pass
-// 4.70 ms (1,730); project backward at 25,600 x 6,144 0.73 ms (1,770).  In one
+// 129,280 x 5,120, back to back: loss 1.49 ms (1,810 TFLOP/s), its backward pass
+// 4.68 ms (1,740); project backward at 25,600 x 6,144 0.72 ms (1,790).  In one
 // short launch the tensor pipe is active 80-83% of the cycles.  256 x 256 tiles on
 // pairs: a pair takes in 64 KB per 512 cycles of MMA, two thirds of what two
 // single CTAs with 128 x 256 tiles would.  Six stages: five or seven differ by 1-2%.
@@ -623,38 +623,48 @@ k_grad(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtenso
     }
 }
 
-// (2,048 rows of 1,010 groups: 16 MB from L2, about 8 us.)
-// loss and lse of each row from the column groups' (maximum, sum) pairs, in
-// column order within each of the block's eight slices of the groups, then the
-// slices in order.
-__global__ void k_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel,
-                               const int32_t* labels, int vocab, float* loss, float* lse,
-                               uint32_t* err) {
+// loss and lse of each row from the column groups' (maximum, sum) pairs: 32 rows a
+// block, each of its slices a contiguous share of the groups in column order, in
+// batches whose loads leave together, then the slices in order.  2,048 rows of 1,010
+// groups, 16 MB from L2: the loss takes 1.49 ms; with the groups taken one by one,
+// each behind the exponentials of the one before, 1.52.
+constexpr int kCombineSlices = 16, kCombineBatch = 16;
+
+__device__ __forceinline__ void add_pair(float& mx, float& sum, float2 p) {
+    const float nm = fmaxf(mx, p.x);
+    const float b = nm == -INFINITY ? 0.f : nm;
+    sum = sum * expf(mx - b) + p.y * expf(p.x - b);
+    mx = nm;
+}
+__global__ void __launch_bounds__(32 * kCombineSlices)
+k_loss_combine(const float2* part, int groups, int64_t T, const float* zlabel, const int32_t* labels,
+               int vocab, float* loss, float* lse, uint32_t* err) {
     pdl_wait();
-    __shared__ float2 sm[8][32];
+    __shared__ float2 sm[kCombineSlices][32];
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * 32 + lane;
     float mx = -INFINITY, sum = 0.f;
     if (t < T) {
-        const int lo = sl * groups / 8, hi = (sl + 1) * groups / 8;
-        for (int g = lo; g < hi; ++g) {
-            const float2 p = part[(int64_t)g * T + t];
-            const float nm = fmaxf(mx, p.x);
+        const int lo = sl * groups / kCombineSlices, hi = (sl + 1) * groups / kCombineSlices;
+        for (int g = lo; g < hi; g += kCombineBatch) {
+            float2 p[kCombineBatch];
+            float nm = mx;
+#pragma unroll
+            for (int u = 0; u < kCombineBatch; ++u)
+                p[u] = g + u < hi ? part[(int64_t)(g + u) * T + t] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < kCombineBatch; ++u) nm = fmaxf(nm, p[u].x);
             const float b = nm == -INFINITY ? 0.f : nm;
-            sum = sum * expf(mx - b) + p.y * expf(p.x - b);
+            sum *= expf(mx - b);
+#pragma unroll
+            for (int u = 0; u < kCombineBatch; ++u) sum += p[u].y * expf(p[u].x - b);
             mx = nm;
         }
     }
     sm[sl][lane] = make_float2(mx, sum);
     __syncthreads();
     if (sl || t >= T) return;
-    for (int k = 1; k < 8; ++k) {
-        const float2 p = sm[k][lane];
-        const float nm = fmaxf(mx, p.x);
-        const float b = nm == -INFINITY ? 0.f : nm;
-        sum = sum * expf(mx - b) + p.y * expf(p.x - b);
-        mx = nm;
-    }
+    for (int k = 1; k < kCombineSlices; ++k) add_pair(mx, sum, sm[k][lane]);
     const float l = mx + logf(sum);
     const int y = labels[t];
     if (y >= vocab) atomicOr(err, kErrBounds);
@@ -806,7 +816,7 @@ cudaError_t launch_loss_combine(const float2* part, int groups, int64_t T, const
                                 const int32_t* labels, int vocab, float* loss, float* lse,
                                 uint32_t* err, cudaStream_t s) {
     void* args[] = {&part, &groups, &T, &zlabel, &labels, &vocab, &loss, &lse, &err};
-    return pdl_launch((void*)k_loss_combine, dim3((unsigned)((T + 31) / 32)), dim3(256), args, s);
+    return pdl_launch((void*)k_loss_combine, dim3((unsigned)((T + 31) / 32)), dim3(32 * kCombineSlices), args, s);
 }
 
 cudaError_t launch_sum_splits(const float* acc, int splits, int64_t n, const float* unit, uint16_t* out,
