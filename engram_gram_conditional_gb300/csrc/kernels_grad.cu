@@ -56,7 +56,8 @@ constexpr int kChunk = 64 * kBK * 2;      // 8 KB: 64 MN elements x 64 k of an M
 // An epilogue warp turns 32 rows x 64 BF16 of a tile from a row per lane into
 // whole 128-byte lines through a box of shared memory.  (16-byte stores of a row
 // per lane, straight to memory, took 4.5 us per tile where the MMAs of a
-// 384-long reduction take 1.6.)
+// 384-long reduction take 1.6; bulk copies of the boxes make 16 tokens' project
+// backward 6% faster, 333 tokens' no different and the loss's backward 0.5% slower.)
 constexpr int kBox = 32 * 64 * 2;
 
 // Shared memory of each variant.
