@@ -10,7 +10,7 @@
 // longer than a chunk: no atomics on values, so the same sums on every run.
 // Measured (GB300, copy bandwidth 6.77 TB/s): 8,192 tokens x 4 branches x 5,120:
 // 100 us - sort 15, sums 74 (5.6 TB/s), joins 14 (cold caches); 50,032 x 24 rows
-// of 256 from 64 million: 273 us - sort 68, sums 181 (5.8 TB/s), joins 21.
+// of 256 from 64 million: 271 us - sort 66, sums 181 (5.8 TB/s), joins 21.
 #include <algorithm>
 
 #include "grad_internal.h"
@@ -672,12 +672,12 @@ k_embed_sum(const EmbedSum a) {
 
 // The rows of the segments that left partial sums: the tail of the chunk in which
 // one begins and the heads of the chunks after it, added in order.  A block looks
-// for them in `look` chunks (at most kJoinMost), then each group of `lanes` threads
-// takes one after the other; one of more than kJoinAlone parts (a hot id) is added
-// by the whole block, each group a contiguous share, then the shares in order.
-// (3 million rows of 8 columns, 200,000 ids: 484 us with whole warps as groups,
-// 397 so.  Looking for the segments before the sums have ended takes blocks from
-// them: 275 us against 271 at 50,032 x 24 rows of 256.)
+// for them in `look` chunks (at most kJoinMost), then each group of kLanes threads
+// (as many as a row has columns by eight, 32 at most) takes one after the other;
+// one of more than kJoinAlone parts (a hot id) is added by the whole block, each
+// group a contiguous share, then the shares in order.  (3 million rows of 8
+// columns, 200,000 ids: 484 us with whole warps as groups, 391 so; at 50,032 x 24
+// rows of 256 a group's size known only at run time costs 4 us of 271.)
 constexpr int kJoinMost = 64, kJoinAlone = 32;
 
 __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int64_t p0, int64_t p1, int col,
@@ -692,14 +692,15 @@ __device__ __forceinline__ void add_parts(const EmbedSum& a, int64_t chunk, int6
     }
 }
 
+template <int kLanes>
 __global__ void __launch_bounds__(256, 3)
 k_embed_join(const EmbedSum a, int64_t chunks, int look) {
-    pdl_wait();
-    __shared__ float sm[256][9];
+    constexpr int kGroups = 256 / kLanes;
+    __shared__ float sm[kGroups][kLanes][9];
     __shared__ int parts_of[kJoinMost];
     __shared__ uint32_t seg_of[kJoinMost];
-    const int groups = 256 / a.lanes, g = threadIdx.x / a.lanes;
-    const int col = ((int)blockIdx.y * a.lanes + (int)threadIdx.x % a.lanes) * 8;
+    const int lane = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
+    const int col = ((int)blockIdx.y * kLanes + lane) * 8;
     const int64_t first = (int64_t)blockIdx.x * look;
     if ((int)threadIdx.x < look) {
         const int64_t nv = *a.n_valid;
@@ -722,7 +723,8 @@ k_embed_join(const EmbedSum a, int64_t chunks, int look) {
         seg_of[threadIdx.x] = seg;
     }
     __syncthreads();
-    for (int c = g; c < look; c += groups) {
+    pdl_wait();  // for the sums; the places were there before their kernel's blocks began
+    for (int c = g; c < look; c += kGroups) {
         const int parts = parts_of[c];
         if (parts == 0 || parts > kJoinAlone || col >= a.dim) continue;
         float acc[8] = {};
@@ -733,14 +735,15 @@ k_embed_join(const EmbedSum a, int64_t chunks, int look) {
         const int64_t parts = parts_of[c];
         if (parts <= kJoinAlone) continue;
         float acc[8] = {};
-        add_parts(a, first + c, parts * g / groups, parts * (g + 1) / groups, col, acc);
+        add_parts(a, first + c, parts * g / kGroups, parts * (g + 1) / kGroups, col, acc);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sm[threadIdx.x][j] = acc[j];
+        for (int j = 0; j < 8; ++j) sm[g][lane][j] = acc[j];
         __syncthreads();
         if (g == 0 && col < a.dim) {
-            for (int x = 1; x < groups; ++x)
+#pragma unroll 8
+            for (int x = 1; x < kGroups; ++x)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] += sm[x * a.lanes + threadIdx.x][j];
+                for (int j = 0; j < 8; ++j) acc[j] += sm[x][lane][j];
             put_row(a, seg_of[c], col, acc);
         }
         __syncthreads();
@@ -836,7 +839,13 @@ cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {
     // about four blocks per SM
     const int64_t slices = a.slices, want = chunks * slices / (device_sm_count() * 4) + 1;
     const int look = (int)std::min<int64_t>(kJoinMost, std::max<int64_t>(8, want));
-    return pdl_launch(k_embed_join, dim3((unsigned)((chunks + look - 1) / look), (unsigned)slices), dim3(256), 0, s,
+    auto join = a.lanes == 32   ? k_embed_join<32>
+                : a.lanes == 16 ? k_embed_join<16>
+                : a.lanes == 8  ? k_embed_join<8>
+                : a.lanes == 4  ? k_embed_join<4>
+                : a.lanes == 2  ? k_embed_join<2>
+                                : k_embed_join<1>;
+    return pdl_launch(join, dim3((unsigned)((chunks + look - 1) / look), (unsigned)slices), dim3(256), 0, s,
                       a, chunks, look);
 }
 
