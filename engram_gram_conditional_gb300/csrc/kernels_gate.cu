@@ -981,13 +981,14 @@ int one_pass_cluster(int d, Bytes bytes, int* stages) {
     return 0;
 }
 
-template <class F>
-cudaError_t one_pass_launch(F kern, const GateTrain& a, int cs, int stages, int stage_bytes, int* clusters,
+template <auto kKernel>
+cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_bytes, int* clusters,
                             cudaStream_t s) {
     const int per = (a.d / 256 + cs - 1) / cs;
     const int smem = (kFusedFixed + 127) / 128 * 128 + stages * stage_bytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static const cudaError_t allowed =
+        cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (allowed != cudaSuccess) return allowed;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -996,27 +997,35 @@ cudaError_t one_pass_launch(F kern, const GateTrain& a, int cs, int stages, int 
     attr[1].val.clusterDim.x = cs;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    // (as many clusters as are resident at once: larger ones leave SMs of a GPC over)
-    int resident = device_sm_count();
+    // as many clusters as are resident at once (larger ones leave SMs of a GPC over),
+    // asked for when the shape changes
+    static thread_local struct { int cs, per, smem, clusters; } known = {};
     cfg.gridDim = dim3(device_sm_count() / cs * cs);
     cfg.blockDim = dim3((per + 2) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr + 1;
     cfg.numAttrs = 1;
-    if (cs > 1 && (e = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg)) != cudaSuccess) return e;
-    *clusters = (int)std::min<int64_t>(a.T, std::max(1, std::min(resident, device_sm_count() / cs)));
+    if (known.cs != cs || known.per != per || known.smem != smem) {
+        int resident = device_sm_count();
+        if (cs > 1) {
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&resident, kKernel, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        known = {cs, per, smem, std::max(1, std::min(resident, device_sm_count() / cs))};
+    }
+    *clusters = (int)std::min<int64_t>(a.T, known.clusters);
     cfg.gridDim = dim3(*clusters * cs);
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, stages, cs, std::min(2, stages - 2));
+    return cudaLaunchKernelEx(&cfg, kKernel, a, stages, cs, std::min(2, stages - 2));
 }
 
 template <int kSaved, int kHc>
 cudaError_t fused_launch(const GateTrain& a, int cs, int stages, int* shares, cudaStream_t s) {
     const int bytes = fused_stage_bytes<kSaved>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
-    return a.hc == kHc ? one_pass_launch(k_gate_backward_fused<kSaved, kHc, true>, a, cs, stages, bytes, shares, s)
-                       : one_pass_launch(k_gate_backward_fused<kSaved, kHc, false>, a, cs, stages, bytes, shares, s);
+    return a.hc == kHc ? one_pass_launch<k_gate_backward_fused<kSaved, kHc, true>>(a, cs, stages, bytes, shares, s)
+                       : one_pass_launch<k_gate_backward_fused<kSaved, kHc, false>>(a, cs, stages, bytes, shares, s);
 }
 
 template <bool kF32Kv, int kHc>
@@ -1024,8 +1033,8 @@ cudaError_t ckpt_launch(const GateTrain& a, int cs, int stages, cudaStream_t s) 
     const int bytes = ckpt_stage_bytes<kF32Kv>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
     int clusters;
     return a.hc == kHc
-               ? one_pass_launch(k_gate_checkpoint_fused<kF32Kv, kHc, true>, a, cs, stages, bytes, &clusters, s)
-               : one_pass_launch(k_gate_checkpoint_fused<kF32Kv, kHc, false>, a, cs, stages, bytes, &clusters, s);
+               ? one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, true>>(a, cs, stages, bytes, &clusters, s)
+               : one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, false>>(a, cs, stages, bytes, &clusters, s);
 }
 
 template <bool kF32Kv>
