@@ -68,7 +68,7 @@ cudaError_t launch_grad_lse(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_dz(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 cudaError_t launch_grad_products(GradArgs& a, const CUtensorMap* tm, cudaStream_t s);
 // ---- the loss's logits of at most kFewTokens tokens (kernels_few.cu) ----
-constexpr int kFewTokens = 64;
+constexpr int kFewTokens = 16;
 struct FewArgs {
     int T, kb;             // tokens, blocks of 64 columns
     int rows, vocab;       // vocabulary rows of the piece, of the head

@@ -1,12 +1,16 @@
-// The loss's logits of a few tokens (at most 64, sm_103a): softmax statistics,
-// or dz of a piece of the vocabulary.
+// The loss's logits of at most 16 tokens (sm_103a): softmax statistics, or dz of a
+// piece of the vocabulary.
 //
 // With so few tokens the head's bytes are the whole cost, so the product is
-// turned round: 128 rows of the head are the M of a tcgen05.mma (one CTA), the
-// tokens, padded to 16, 32 or 64, its N - an MMA that takes a fraction of its
-// operand's way through memory.  (The 256 x 256 tiles of kernels_grad.cu
-// compute 256 rows of tokens whatever their number: 16 tokens over 129,280 x
-// 5,120 took 255 us with them, and take 209 here, 93% of the copy bandwidth.)  Every CTA owns a contiguous range of the
+// turned round: 128 rows of the head are the M of a tcgen05.mma (one CTA), 16
+// tokens its N - an MMA that takes a fraction of its operand's way through
+// memory.  (The 256 x 256 tiles of kernels_grad.cu compute 256 rows of tokens
+// whatever their number: over 129,280 x 5,120 one token's loss takes 323 us with
+// them, 8 tokens' 287 and 16 tokens' 222, and 206 here, 95% of the copy bandwidth;
+// 32 and 64 tokens as N take 214 and 243 against 223 and 228 with the tiles, and
+// over 32,000 x 2,048 39 and 68 against 33 and 34: N is 16 at most.  The gradient
+// of 1, 8 and 16 tokens: 793, 751 and 696 us with the tiles, 677, 683 and 687
+// here.)  Every CTA owns a contiguous range of the
 // vocabulary, in units of 32 rows, and streams it once through a ring of TMA
 // stages of 64 columns; a thread of the epilogue owns a vocabulary row of the
 // tile and keeps each token's running maximum and sum over all its rows, so
@@ -27,10 +31,10 @@ constexpr int kThreads = 192;
 constexpr int kWarpTma = 4, kWarpMma = 5;
 constexpr int kUnit = 32;               // vocabulary rows that a CTA's range is a multiple of
 constexpr int kRowsBytes = kBM * kBK * 2;  // 16 KB: 128 rows x 64
+constexpr int kN = kFewTokens;          // tokens of an MMA
 constexpr int kSegment = 16;            // k-blocks per accumulator (as in kernels_grad.cu)
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int kN>
 struct Layout {
     static constexpr int kStage = kRowsBytes + kN * kBK * 2;
     static constexpr int kStages = 216 * 1024 / kStage;
@@ -44,7 +48,6 @@ struct Layout {
     static constexpr uint32_t kTmemCols = 2 * kN;  // two accumulators (a power of two, at least 32)
 };
 
-template <int kN>
 __host__ __device__ constexpr uint32_t few_idesc() {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
 }
@@ -70,11 +73,11 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 // kDz: dz of vocabulary rows [v0, v0 + rows); else the statistics of all rows.
 // tmV: head rows in boxes of 128 x 64, tmU: of 32 x 64 (a range's last tile),
 // tmX: x in boxes of kN x 64.
-template <int kN, bool kDz>
+template <bool kDz>
 __global__ void __launch_bounds__(kThreads, 1)
 k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmU,
       const __grid_constant__ CUtensorMap tmX, const FewArgs a) {
-    using L = Layout<kN>;
+    using L = Layout;
     constexpr int kStages = L::kStages;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -172,7 +175,7 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
                     const uint64_t ad = sdesc_sw128(sv), bd = sdesc_sw128(sv + kRowsBytes);
 #pragma unroll
                     for (int k = 0; k < kBK / 16; ++k)
-                        umma_f16kind(d_tmem, ad + 2ull * k, bd + 2ull * k, few_idesc<kN>(), (seg != 0) || (k != 0));
+                        umma_f16kind(d_tmem, ad + 2ull * k, bd + 2ull * k, few_idesc(), (seg != 0) || (k != 0));
                     umma_commit(empty(s));
                     if (++seg == kSegment || kb + 1 == kb_all) {
                         umma_commit(tfull(use & 1));
@@ -201,15 +204,11 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
                 if (!ok && lane == 0) fail();
                 tc_fence_after();
                 const uint32_t taddr = tmem_base + (uint32_t)((use & 1) * kN) + ((uint32_t)(warp * 32) << 16);
+                uint32_t r[kN];
+                tmem_ld16(taddr, r);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < kN; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(taddr + (uint32_t)c, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        z[c + j] = seg ? z[c + j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
-                }
+                for (int j = 0; j < kN; ++j) z[j] = seg ? z[j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tempty(use & 1));
@@ -235,6 +234,7 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
                     }
                     out[t * 64] = (uint16_t)(bf16x2_pack_rn(d, d) & 0xFFFFu);
                 }
+                for (int t = kN; t < 64; ++t) out[t * 64] = 0;
             } else if (in) {
 #pragma unroll
                 for (int t = 0; t < kN; ++t) {
@@ -276,16 +276,16 @@ k_few(const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorM
     }
 }
 
-template <int kN, bool kDz>
+template <bool kDz>
 cudaError_t launch(const FewArgs& a, const uint16_t* x, const uint16_t* head, int64_t head_rows, int dim,
                    int groups, cudaStream_t s) {
     CUtensorMap tmV, tmU, tmX;
     cudaError_t e = make_tma_16bit(&tmV, head, head_rows, dim, kBM, false);
     if (e == cudaSuccess) e = make_tma_16bit(&tmU, head, head_rows, dim, kUnit, false);
     if (e == cudaSuccess) e = make_tma_16bit(&tmX, x, a.T, dim, kN, false);
-    auto kern = k_few<kN, kDz>;
+    auto kern = k_few<kDz>;
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kN>::kSmem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -293,7 +293,7 @@ cudaError_t launch(const FewArgs& a, const uint16_t* x, const uint16_t* head, in
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(groups);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Layout<kN>::kSmem;
+    cfg.dynamicSmemBytes = Layout::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -307,14 +307,11 @@ int few_groups(int64_t rows) {
 }
 
 cudaError_t launch_few_lse(const FewArgs& a, const uint16_t* x, const uint16_t* head, int dim, cudaStream_t s) {
-    const int groups = few_groups(a.rows);
-    if (a.T <= 16) return launch<16, false>(a, x, head, a.vocab, dim, groups, s);
-    if (a.T <= 32) return launch<32, false>(a, x, head, a.vocab, dim, groups, s);
-    return launch<64, false>(a, x, head, a.vocab, dim, groups, s);
+    return launch<false>(a, x, head, a.vocab, dim, few_groups(a.rows), s);
 }
 
 cudaError_t launch_few_dz(const FewArgs& a, const uint16_t* x, const uint16_t* head, int dim, cudaStream_t s) {
-    return launch<64, true>(a, x, head, a.vocab - a.v0, dim, few_groups(a.rows), s);
+    return launch<true>(a, x, head, a.vocab - a.v0, dim, few_groups(a.rows), s);
 }
 
 }  // namespace engram
