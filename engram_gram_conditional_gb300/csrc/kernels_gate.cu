@@ -221,7 +221,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[kN], int lane) {
 
 // kExact: hc == kHc (no branch is left out).
 template <int kSaved, int kHc, bool kExact>
-__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
+__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, kHc == 1 ? 2 : 1)
 k_gate_backward_fused(const GateTrain a, int stages, int cs, int lag) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSums = 4 * kHc;
@@ -526,7 +526,7 @@ __device__ __forceinline__ uint2 encode_mx8(const f32x2 (&v)[4], uint32_t& expon
 }
 
 template <bool kF32Kv, int kHc, bool kExact>
-__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, 1)
+__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, kHc == 1 ? 2 : 1)
 k_gate_checkpoint_fused(const GateTrain a, int stages, int cs, int lag) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSums = 4 * kHc;  // (three used per branch)
@@ -965,8 +965,13 @@ k_gate_backward_weights(const GateTrain a, int shares) {
 // bytes(cols) bytes; 0 if no cluster holds two.  The smallest cluster that does:
 // at hc 4, d 5,120 two CTAs with two stages of fp32 kv and gradient (and no lag)
 // 111 us, four with four stages 144, since half as many warps share an SM's
-// work.  The lag is what the stages allow beside one that fills: none of two, one
-// of three, two of four or more.
+// work.  Where four stages fit half of an SM's shared memory, they take no more than
+// that, so that two CTAs share the SM if the registers allow (hc 1, d 5,120: forward
+// with fp32 kv 57 -> 40 us, backward from the checkpoint 54 -> 38; hc 4, d 1,024:
+// 25 -> 16 with BF16 kv, 30 -> 24; hc 2, d 5,120 from the checkpoint 72 -> 74):
+// a token of few bytes is bound by the latency of its cluster's exchange.  The lag
+// is what the stages allow beside one that fills: none of two, one of three, two of
+// four or more.
 template <class Bytes>
 int one_pass_cluster(int d, Bytes bytes, int* stages) {
     const int groups = d / 256;
@@ -974,7 +979,8 @@ int one_pass_cluster(int d, Bytes bytes, int* stages) {
         const int per = (groups + cs - 1) / cs;
         const int n = (227 * 1024 - kFusedFixed - 128) / bytes(per * 256);
         if (per <= kFusedMaxWarps && n >= 2) {
-            *stages = std::min(n, 6);
+            const int half = (113 * 1024 - kFusedFixed - 128) / bytes(per * 256);
+            *stages = std::min(half >= 4 ? half : n, 6);
             return cs;
         }
     }
@@ -982,7 +988,7 @@ int one_pass_cluster(int d, Bytes bytes, int* stages) {
 }
 
 template <auto kKernel>
-cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_bytes, int* clusters,
+cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_bytes, int most, int* clusters,
                             cudaStream_t s) {
     const int per = (a.d / 256 + cs - 1) / cs;
     const int smem = (kFusedFixed + 127) / 128 * 128 + stages * stage_bytes;
@@ -998,7 +1004,7 @@ cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_by
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     // as many clusters as are resident at once (larger ones leave SMs of a GPC over),
-    // asked for when the shape changes
+    // asked for when the shape changes, and no more than `most`
     static thread_local struct { int cs, per, smem, clusters; } known = {};
     cfg.gridDim = dim3(device_sm_count() / cs * cs);
     cfg.blockDim = dim3((per + 2) * 32);
@@ -1007,14 +1013,15 @@ cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_by
     cfg.attrs = attr + 1;
     cfg.numAttrs = 1;
     if (known.cs != cs || known.per != per || known.smem != smem) {
-        int resident = device_sm_count();
-        if (cs > 1) {
-            const cudaError_t e = cudaOccupancyMaxActiveClusters(&resident, kKernel, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-        known = {cs, per, smem, std::max(1, std::min(resident, device_sm_count() / cs))};
+        int resident = 1;
+        const cudaError_t e =
+            cs > 1 ? cudaOccupancyMaxActiveClusters(&resident, kKernel, &cfg)
+                   : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kKernel, (per + 2) * 32, smem);
+        if (e != cudaSuccess) return e;
+        if (cs == 1) resident *= device_sm_count();
+        known = {cs, per, smem, std::max(1, resident)};
     }
-    *clusters = (int)std::min<int64_t>(a.T, known.clusters);
+    *clusters = (int)std::min<int64_t>(a.T, std::min(known.clusters, most));
     cfg.gridDim = dim3(*clusters * cs);
     cfg.attrs = attr;
     cfg.numAttrs = cs > 1 ? 2 : 1;
@@ -1024,8 +1031,10 @@ cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_by
 template <int kSaved, int kHc>
 cudaError_t fused_launch(const GateTrain& a, int cs, int stages, int* shares, cudaStream_t s) {
     const int bytes = fused_stage_bytes<kSaved>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
-    return a.hc == kHc ? one_pass_launch<k_gate_backward_fused<kSaved, kHc, true>>(a, cs, stages, bytes, shares, s)
-                       : one_pass_launch<k_gate_backward_fused<kSaved, kHc, false>>(a, cs, stages, bytes, shares, s);
+    const int most = gate_backward_shares(a.T, a.d);
+    return a.hc == kHc
+               ? one_pass_launch<k_gate_backward_fused<kSaved, kHc, true>>(a, cs, stages, bytes, most, shares, s)
+               : one_pass_launch<k_gate_backward_fused<kSaved, kHc, false>>(a, cs, stages, bytes, most, shares, s);
 }
 
 template <bool kF32Kv, int kHc>
@@ -1033,8 +1042,8 @@ cudaError_t ckpt_launch(const GateTrain& a, int cs, int stages, cudaStream_t s) 
     const int bytes = ckpt_stage_bytes<kF32Kv>(a.hc, (a.d / 256 + cs - 1) / cs * 256);
     int clusters;
     return a.hc == kHc
-               ? one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, true>>(a, cs, stages, bytes, &clusters, s)
-               : one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, false>>(a, cs, stages, bytes, &clusters, s);
+               ? one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, true>>(a, cs, stages, bytes, 1 << 30, &clusters, s)
+               : one_pass_launch<k_gate_checkpoint_fused<kF32Kv, kHc, false>>(a, cs, stages, bytes, 1 << 30, &clusters, s);
 }
 
 template <bool kF32Kv>
@@ -1084,7 +1093,7 @@ cudaError_t launch_gate_checkpoint(const GateTrain& a, bool kv_f32, cudaStream_t
 
 int gate_backward_shares(int64_t T, int d) {
     const int blocks = (d / 8 + 127) / 128;
-    // (the fused kernel's clusters are no more than the SMs)
+    // (the fused kernel launches no more clusters than these)
     return (int)std::max<int64_t>(1, std::min<int64_t>(T, device_sm_count() * std::max(1, 4 / blocks)));
 }
 
