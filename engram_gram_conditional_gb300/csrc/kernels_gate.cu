@@ -526,7 +526,7 @@ __device__ __forceinline__ uint2 encode_mx8(const f32x2 (&v)[4], uint32_t& expon
 }
 
 template <bool kF32Kv, int kHc, bool kExact>
-__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, kHc == 1 ? 2 : 1)
+__global__ void __launch_bounds__((kFusedMaxWarps + 2) * 32, kHc <= 2 ? 2 : 1)
 k_gate_checkpoint_fused(const GateTrain a, int stages, int cs, int lag) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kSums = 4 * kHc;  // (three used per branch)
@@ -965,11 +965,12 @@ k_gate_backward_weights(const GateTrain a, int shares) {
 // bytes(cols) bytes; 0 if no cluster holds two.  The smallest cluster that does:
 // at hc 4, d 5,120 two CTAs with two stages of fp32 kv and gradient (and no lag)
 // 111 us, four with four stages 144, since half as many warps share an SM's
-// work.  Where four stages fit half of an SM's shared memory, they take no more than
+// work.  Where three stages fit half of an SM's shared memory, they take no more than
 // that, so that two CTAs share the SM if the registers allow (hc 1, d 5,120: forward
-// with fp32 kv 57 -> 40 us, backward from the checkpoint 54 -> 38; hc 4, d 1,024:
-// 25 -> 16 with BF16 kv, 30 -> 24; hc 2, d 5,120 from the checkpoint 72 -> 74):
-// a token of few bytes is bound by the latency of its cluster's exchange.  The lag
+// with fp32 kv 57 -> 40 us, backward from the checkpoint 54 -> 38; hc 2, d 5,120:
+// forward with BF16 kv 61 -> 44; hc 4, d 1,024: with fp32 kv 26 -> 17, from the
+// checkpoint 30 -> 24; hc 3, d 3,840 from the checkpoint 71 -> 73): a token of few
+// bytes is bound by the latency of its cluster's exchange.  The lag
 // is what the stages allow beside one that fills: none of two, one of three, two of
 // four or more.
 template <class Bytes>
@@ -980,7 +981,7 @@ int one_pass_cluster(int d, Bytes bytes, int* stages) {
         const int n = (227 * 1024 - kFusedFixed - 128) / bytes(per * 256);
         if (per <= kFusedMaxWarps && n >= 2) {
             const int half = (113 * 1024 - kFusedFixed - 128) / bytes(per * 256);
-            *stages = std::min(half >= 4 ? half : n, 6);
+            *stages = std::min(half >= 3 ? half : n, 6);
             return cs;
         }
     }
