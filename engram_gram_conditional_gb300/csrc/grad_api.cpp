@@ -70,7 +70,7 @@ EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
     w.hist = c.take<uint32_t>(blocks * bins);
     w.digit_total = c.take<uint32_t>(bins);
     w.block_heads = c.take<uint32_t>(blocks);
-    w.barrier = c.take<uint32_t>(1);
+    w.barrier = c.take<uint32_t>(2);
     w.n_valid = c.take<uint32_t>(1);
     w.count = c.take<uint32_t>(1);
     w.segpos = c.take<uint32_t>(n);
@@ -309,6 +309,7 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
     a.digit_total = w.digit_total;
     a.block_heads = w.block_heads;
     a.barrier = w.barrier;
+    a.failed = w.barrier + 1;
     a.n_valid = w.n_valid;
     a.segpos = w.segpos;
     a.seg_start = w.seg_start;
@@ -316,6 +317,7 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
     a.count = d_count ? d_count : w.count;
     a.err = ctx->d_err;
     a.wait_limit_ns = ctx->wait_limit_ns;
+    a.starve = ctx->starve_b;
     e = launch_embed_sort(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "embed sort launch");
     EmbedSum u{};
@@ -324,6 +326,7 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
     u.seg_start = w.seg_start;
     u.unique = a.unique;
     u.n_valid = w.n_valid;
+    u.failed = a.failed;
     u.dout = d_dout;
     u.dim = (int)dim;
     u.copies = (int)copies;

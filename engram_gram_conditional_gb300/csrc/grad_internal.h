@@ -108,7 +108,8 @@ struct EmbedSort {
     uint32_t* hist;          // [2^digit_bits][blocks]
     uint32_t* digit_total;   // [2^digit_bits]
     uint32_t* block_heads;   // [blocks]
-    uint32_t* barrier;
+    uint32_t* barrier;       // arrivals; right behind it:
+    uint32_t* failed;        // set where a wait ran out: the results are not whole
     uint32_t* n_valid;       // ids that are rows
     uint32_t* segpos;        // [n] segment of each sorted place
     uint32_t* seg_start;     // [n + 1] first place of each segment
@@ -116,6 +117,7 @@ struct EmbedSort {
     uint32_t* count;         // segments
     uint32_t* err;
     long long wait_limit_ns;
+    int starve;              // test hook: one block keeps its arrivals at the barriers back
 };
 int embed_sort_blocks(int64_t n);
 void embed_sort_digits(uint64_t rows, int* passes, int* bits);
@@ -123,7 +125,7 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s);
 // The rows' sums: grad[segment or, dense, its id] = scale x the sum of its rows of dout.
 struct EmbedSum {
     const uint2* sorted;     // (id, position)
-    const uint32_t *segpos, *seg_start, *unique, *n_valid;
+    const uint32_t *segpos, *seg_start, *unique, *n_valid, *failed;
     const uint16_t* dout;    // bf16 [n][copies][dim]
     int dim, copies;
     float scale;

@@ -64,11 +64,14 @@ constexpr int kSmallSort = kSortThreads * 8 * 4;  // keys of the one-cluster sor
 // A barrier of the cooperative launch's blocks in two halves, so that a block can
 // work between them; the wait is bounded: false on a time-out.  The block's barrier
 // orders its writes before the release, and the acquire before what it reads next.
+// A block whose wait ran out leaves the sort unfinished: it says so in *a.failed, and
+// the kernels behind the sort, whose loops and addresses come from its results, then
+// take it that there are no ids.
 __device__ __forceinline__ void grid_arrive(const EmbedSort& a) {
     __syncthreads();
-    if (threadIdx.x == 0) {
+    const bool starved = a.starve && blockIdx.x + 1 == gridDim.x;
+    if (threadIdx.x == 0 && !starved)
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.barrier) : "memory");
-    }
 }
 __device__ __forceinline__ bool grid_wait(const EmbedSort& a, uint32_t& phase, int* flag) {
     if (threadIdx.x == 0) {
@@ -78,6 +81,7 @@ __device__ __forceinline__ bool grid_wait(const EmbedSort& a, uint32_t& phase, i
         while (ld_acquire_u32(a.barrier) < want) {
             if ((++spin & 63u) == 0u && (long long)(globaltimer() - t0) > a.wait_limit_ns) {
                 atomicOr(a.err, kErrTimeout);
+                *a.failed = 1u;
                 *flag = 1;
                 break;
             }
@@ -531,6 +535,7 @@ k_embed_sort_small(const EmbedSort a) {
     }
     if (i0 == 0) {
         *a.count = all;
+        *a.failed = 0u;  // (no wait of this kernel is bounded)
         if (all == 0) *a.n_valid = a.seg_start[0] = 0u;
     }
     cluster_sync();  // no CTA exits while another reads its shared memory
@@ -546,6 +551,12 @@ k_embed_sort_small(const EmbedSort a) {
 // order in which blocks run, and a hot id's rows are spread over as many threads
 // as a cold one's.
 constexpr int kSumBatch = 8;  // rows loaded before they are added
+
+// Ids that are rows; none if the sort did not finish.
+__device__ __forceinline__ int64_t valid_ids(const EmbedSum& a) {
+    const uint32_t n = *a.n_valid, failed = *a.failed;
+    return failed ? 0 : n;
+}
 
 __device__ __forceinline__ void put_row(const EmbedSum& a, uint32_t seg, int col,
                                         const float (&acc)[8]) {
@@ -575,7 +586,7 @@ k_embed_sum(const EmbedSum a) {
     const int64_t work = ((int64_t)blockIdx.x * 256 + threadIdx.x) / a.lanes;
     const int64_t chunk = work / a.slices;
     const int col = ((int)(work - chunk * a.slices) * a.lanes + l) * 8;
-    const int64_t nv = *a.n_valid;
+    const int64_t nv = valid_ids(a);
     int64_t lo = chunk * a.rows_per_chunk, hi = min(lo + a.rows_per_chunk, nv);
     const int beyond = a.rows_per_chunk / 2;
     bool began_before = false, goes_on = false;
@@ -703,7 +714,7 @@ k_embed_join(const EmbedSum a, int64_t chunks, int look) {
     const int col = ((int)blockIdx.y * kLanes + lane) * 8;
     const int64_t first = (int64_t)blockIdx.x * look;
     if ((int)threadIdx.x < look) {
-        const int64_t nv = *a.n_valid;
+        const int64_t nv = valid_ids(a);
         const int64_t chunk = first + threadIdx.x;
         const int64_t lo = chunk * a.rows_per_chunk, hi = lo + a.rows_per_chunk;
         int parts = 0;
@@ -807,7 +818,7 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
     const int blocks = embed_sort_blocks(a.n);
     const int smem = kSortWarps * (1 << a.digit_bits) * 4 + kSortThreads * kSortBatch * 8;
     cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaMemsetAsync(a.barrier, 0, 4, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(a.barrier, 0, 8, s);  // with *a.failed
     if (e != cudaSuccess) return e;
     EmbedSort copy = a;
     void* args[] = {&copy};

@@ -490,6 +490,8 @@ engram_status engram_embed(engram_ctx* ctx, const void* d_table, int table_forma
  *    (n = T nb, dim = row_dim, copies 1, dout = demb [T][K]).
  *  dense (d_unique NULL, d_count may be): d_grad fp32 [rows][dim]; with
  *    accumulate 0 it is written whole, with 1 the sums are added to it.
+ * Where a wait of the sort runs out (ENGRAM_ETIMEOUT), no row of d_grad is
+ * written but by the clearing of a dense gradient.
  * d_workspace: engram_embed_grad_workspace_bytes(n, rows, dim) bytes. */
 size_t engram_embed_grad_workspace_bytes(int64_t n, uint64_t rows, uint32_t dim);
 engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, const uint32_t* d_ids,
@@ -587,7 +589,9 @@ engram_status engram_ctx_set_wait_limit(engram_ctx* ctx, int64_t ns);
 /* Test hook for the bounded waits: while on, the GEMM kernels issue no wkv
  * loads (the training products and the loss: no loads at all), so the
  * tensor-core issuer's wait for them runs out (after the wait limit) and the
- * call ends with ENGRAM_ETIMEOUT.  Nothing faults or hangs. */
+ * call ends with ENGRAM_ETIMEOUT; so does engram_embed_grad of more than
+ * 32,768 ids, one block of whose sort keeps back its arrivals at the barriers.
+ * Nothing faults or hangs. */
 engram_status engram_debug_starve_operand(engram_ctx* ctx, int on);
 
 /* Message of the calling thread's last error ("" if none). */

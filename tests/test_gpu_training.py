@@ -669,6 +669,54 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_stays_usable():
         s.close()
 
 
+@pytest.mark.parametrize("form", ["sparse", "dense", "accumulate"])
+def test_a_sort_whose_wait_runs_out_writes_no_gradient(form):
+    """The sums behind an unfinished sort touch nothing: neither the outputs nor what lies beside
+    them and the workspace, whatever the workspace held (here words that are no place or row)."""
+    n, rows, dim = 40_000, 3000, 16
+    dense, accumulate = form != "sparse", int(form == "accumulate")
+    ids, dout = ids_like("zipf", n, rows, 3), rnd(4, n, 1, dim)
+    need = eg.engram_embed_grad_workspace_bytes(n, rows, dim)
+    out_rows = rows if dense else n
+    s = make_layer()
+    try:
+        def call(grad, unique, ws):
+            eg.engram_embed_grad(s.ctx, rows, dim, ids.cuda(), n, 1.0, 1, dout.cuda(),
+                                 None if dense else unique[64:], torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                 grad[4:], accumulate, ws[256:])
+
+        def buffers():
+            return (torch.full((out_rows + 8, dim), 7.0, device="cuda"),
+                    torch.full((n + 128,), -5, dtype=torch.int32, device="cuda"),
+                    torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda"))
+
+        grad, unique, ws = buffers()
+        eg.engram_ctx_set_wait_limit(s.ctx, 20_000_000)
+        eg.engram_debug_starve_operand(s.ctx, True)
+        call(grad, unique, ws)
+        with pytest.raises(eg.EngramError) as e:
+            eg.engram_sync(s.ctx)
+        assert e.value.status == eg.ETIMEOUT
+        left = 0.0 if form == "dense" else 7.0
+        assert (grad[4:-4] == left).all() and (grad[:4] == 7.0).all() and (grad[-4:] == 7.0).all()
+        assert (unique[:64] == -5).all() and (unique[-64:] == -5).all()
+        assert (ws[:256] == 0xA5).all() and (ws[-256:] == 0xA5).all()
+        eg.engram_debug_starve_operand(s.ctx, False)
+        eg.engram_ctx_set_wait_limit(s.ctx, 4_000_000_000)
+        grad, unique, _ = buffers()
+        call(grad, unique, ws)  # on what the broken-off call left
+        eg.engram_sync(s.ctx)
+        u, ref, tol = grad_reference(ids.long(), dout, rows, 1.0)
+        got = grad[4:-4].cpu().to(F)
+        if accumulate:
+            ref, tol = ref + 7.0, tol + 2.0 ** -23 * (ref.abs() + 14.0)
+        assert ((got[u if dense else slice(0, u.numel())] - ref).abs() <= tol).all()
+        assert (grad[:4] == 7.0).all() and (grad[-4:] == 7.0).all()
+        assert (ws[:256] == 0xA5).all() and (ws[-256:] == 0xA5).all()
+    finally:
+        s.close()
+
+
 def test_operators_in_a_captured_graph(plain_ctx):
     """Captured once, replayed on new inputs in the same buffers."""
     n, rows, dim, T, V = 20_000, 3000, 64, 100, 1500
