@@ -76,10 +76,7 @@ EmbedWs embed_ws(void* p, int64_t n, uint64_t rows, uint32_t dim) {
     w.segpos = c.take<uint32_t>(n);
     w.seg_start = c.take<uint32_t>(n + 1);
     w.unique = c.take<uint32_t>(n);
-    int64_t chunks = 0;  // of any number of copies
-    for (int copies = 1; copies <= 8; ++copies)
-        chunks = std::max(chunks, ceil_div(n, embed_rows_per_chunk(n, (int)dim, copies)));
-    w.partial = c.take<float>((size_t)chunks * 2 * dim);
+    w.partial = c.take<float>((size_t)embed_most_chunks(n, (int)dim) * 2 * dim);
     w.bytes = c.bytes();
     return w;
 }
@@ -175,6 +172,24 @@ int long_splits(const GradProblem& lng, const GradProblem* shrt) {
     return best;
 }
 
+// fp32 values that the cut products of any batch of at most T tokens park.  The cut
+// follows the tokens in steps of a k-block, and there is none once demb's tiles go
+// 50 times round the pairs: uncut, the last round then costs at most 2% of the mean
+// share, and a cut never makes less than the mean share.
+size_t project_parked(const engram_ctx* ctx, int64_t T) {
+    int64_t most = 0;
+    for (int64_t t = 0; t < T;) {
+        t = std::min<int64_t>(T, t + kBK);
+        const GradProblem demb = product(t, ctx->K, ctx->N, false);
+        const GradProblem dw = product(ctx->N, ctx->K, t, true);
+        if (demb.m_units * (int64_t)demb.n_tiles >= 50 * (int64_t)grad_pairs()) break;
+        // with or without the other product the cut may differ: room for either
+        const int splits = std::max(long_splits(demb, &dw), long_splits(demb, nullptr));
+        if (splits > 1) most = std::max(most, splits * t);
+    }
+    return (size_t)most * ctx->K;
+}
+
 // ---- loss -------------------------------------------------------------------------------
 
 engram_status check_loss(uint32_t vocab, uint32_t dim, int64_t T) {
@@ -188,18 +203,38 @@ int loss_groups(int64_t T, uint32_t vocab) {
     return T <= kFewTokens ? few_groups(vocab) : (int)ceil_div(vocab, kBN) * 2;
 }
 
+// Room for any batch of at most T tokens (few of them may make more pairs than
+// many: their vocabulary is cut finer).
+struct LossWs {
+    float2* part;
+    float* zlabel;
+    size_t bytes;
+};
+LossWs loss_ws(void* p, int64_t T, uint32_t vocab) {
+    const int64_t few = std::min<int64_t>(T, kFewTokens);
+    Carver c(p);
+    LossWs w{};
+    w.part = c.take<float2>((size_t)std::max(loss_groups(T, vocab) * T, loss_groups(few, vocab) * few));
+    w.zlabel = c.take<float>(T);
+    w.bytes = c.bytes();
+    return w;
+}
+
 int loss_group_m(uint32_t dim) {  // M units whose x rows (40 MB) stay in L2 beside the head
     return (int)std::max<int64_t>(1, std::min<int64_t>(64, ((int64_t)40 << 20) / (512 * (int64_t)dim)));
 }
 
 // Vocabulary columns per piece of the backward pass: whole waves of z tiles
-// while dz [T][piece] stays within half of L2, and at least one wave.
+// while dz [T][piece] stays within half of L2, and at least one wave; at least 16
+// tiles for a very long batch.
+constexpr int64_t kPieceBytes = (int64_t)64 << 20, kPieceTiles = 16;
+constexpr int64_t kDzTileBytes = 2 * kBM * kBN * 2;
 int64_t loss_piece(int64_t T, uint32_t vocab) {
     const int64_t units = std::max<int64_t>(1, ceil_div(T, 2 * kBM)), P = grad_pairs();
     const int64_t all = ceil_div(vocab, kBN);
-    const int64_t fit = ((int64_t)64 << 20) / (units * 2 * kBM * kBN * 2);  // tiles within 64 MB
+    const int64_t fit = kPieceBytes / (units * kDzTileBytes);  // tiles within 64 MB
     int64_t waves = fit * units / P;
-    int64_t tiles = std::max<int64_t>(16, waves >= 1 ? waves * P / units : P / units);
+    int64_t tiles = std::max<int64_t>(kPieceTiles, waves >= 1 ? waves * P / units : P / units);
     tiles = std::min(std::max<int64_t>(1, tiles), all);
     return tiles * kBN;
 }
@@ -231,18 +266,38 @@ GradProblem loss_dhead(int64_t T, uint32_t dim, int64_t cols, int64_t piece) {
     q.a_tiled = (int)(piece / 64);
     return q;
 }
-LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim, bool want_dhead) {
-    const int64_t piece = loss_piece(T, vocab), rows = ceil_div(T, 2 * kBM) * 2 * kBM;
+// The cut of dx, before the splits' fp32 dx are held to 64 MB, as dz is.
+int loss_splits(int64_t T, uint32_t vocab, uint32_t dim, bool want_dhead) {
+    const int64_t piece = loss_piece(T, vocab);
     const GradProblem dx = loss_dx(T, dim, piece), dh = loss_dhead(T, dim, piece, piece);
+    return long_splits(dx, want_dhead ? &dh : nullptr);
+}
+// fp32 values of dx that any batch of at most T tokens keeps between pieces (one dx)
+// or parks (as project_parked; with and without the other product the cut may differ).
+size_t loss_parked(int64_t T, uint32_t vocab, uint32_t dim) {
+    const int64_t fit = kPieceBytes / (int64_t)sizeof(float);
+    int64_t most = T * dim;
+    for (int64_t t = 0; t < T && t * dim < fit;) {
+        t = std::min<int64_t>(T, t + kBK);
+        if (ceil_div(t, 2 * kBM) * ceil_div(dim, kBN) >= 50 * (int64_t)grad_pairs()) break;
+        const int splits = std::max(loss_splits(t, vocab, dim, true), loss_splits(t, vocab, dim, false));
+        most = std::max(most, std::min(fit, splits * t * dim));
+    }
+    return (size_t)most;
+}
+// Room for any batch of at most T tokens; acc, the last part, has loss_parked values.
+LossBackWs loss_backward_ws(void* p, int64_t T, uint32_t vocab, uint32_t dim, bool want_dhead) {
+    const int64_t units = ceil_div(T, 2 * kBM), P = grad_pairs();
     LossBackWs w{};
-    // the splits' fp32 dx stay within 64 MB, as dz does
-    const int fit = (int)std::max<int64_t>(1, ((int64_t)64 << 20) / (T * (int64_t)dim * 4));
-    // with and without the other product the cut may differ: room for either
-    w.splits = std::min(fit, long_splits(dx, want_dhead ? &dh : nullptr));
-    const int most = std::max(w.splits, std::min(fit, long_splits(dx, want_dhead ? nullptr : &dh)));
+    const int fit = (int)std::max<int64_t>(1, kPieceBytes / (T * (int64_t)dim * 4));
+    w.splits = std::min(fit, loss_splits(T, vocab, dim, want_dhead));
     Carver c(p);
-    w.dz = c.take<uint16_t>((size_t)rows * piece);
-    w.acc = c.take<float>(most > 1 || piece < vocab ? (size_t)most * T * dim : 0);
+    // units x tiles of dz (loss_piece): whole waves within 64 MB, one at least, or 16
+    // tiles a unit, and no more than the vocabulary has
+    const int64_t waves = std::max<int64_t>(1, kPieceBytes / kDzTileBytes / P) * P;
+    w.dz = reinterpret_cast<uint16_t*>(c.take<uint8_t>(
+        std::min(units * ceil_div(vocab, kBN), std::max(waves, units * kPieceTiles)) * kDzTileBytes));
+    w.acc = c.take<float>(p ? 0 : loss_parked(T, vocab, dim));
     w.bytes = c.bytes();
     return w;
 }
@@ -428,12 +483,8 @@ engram_status engram_gate_backward_checkpoint(const engram_ctx* ctx, int layer,
 
 size_t engram_project_backward_workspace_bytes(const engram_ctx* ctx, int64_t T) {
     if (!ctx || check_T(T) || T == 0) return 0;
-    const GradProblem demb = product(T, ctx->K, ctx->N, false);
-    const GradProblem dw = product(ctx->N, ctx->K, T, true);
-    // with or without the other product the cut may differ: room for either
-    const int splits = std::max(long_splits(demb, &dw), long_splits(demb, nullptr));
     Carver c(nullptr);
-    c.take<float>(splits > 1 ? (size_t)splits * T * ctx->K : 0);
+    c.take<float>(project_parked(ctx, T));
     return c.bytes();
 }
 
@@ -487,10 +538,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
 
 size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim) {
     if (check_loss(vocab, dim, T)) return 0;
-    Carver c(nullptr);
-    c.take<float2>((size_t)loss_groups(T, vocab) * T);
-    c.take<float>(T);
-    return c.bytes();
+    return loss_ws(nullptr, T, vocab).bytes;
 }
 
 engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
@@ -505,17 +553,15 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
         return fail(ENGRAM_EINVAL, "x / head / workspace (16-byte aligned) / labels / loss / lse");
     if ((st = train_device(ctx))) return st;
     const cudaStream_t s = (cudaStream_t)stream;
-    Carver c(d_workspace);
+    const LossWs w = loss_ws(d_workspace, T, vocab);
     const int groups = loss_groups(T, vocab);
-    float2* part = c.take<float2>((size_t)groups * T);
-    float* zlabel = c.take<float>(T);
     cudaError_t e;
     if (T <= kFewTokens) {
         FewArgs f = few_args(ctx, T, vocab, dim);
         f.rows = (int)vocab;
         f.labels = d_labels;
-        f.zlabel = zlabel;
-        f.part = part;
+        f.zlabel = w.zlabel;
+        f.part = w.part;
         e = launch_few_lse(f, d_x, d_head, (int)dim, s);
     } else {
         GradArgs a = grad_args(ctx);
@@ -524,8 +570,8 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
         a.T = T;
         a.vocab = (int)vocab;
         a.labels = d_labels;
-        a.zlabel = zlabel;
-        a.part = part;
+        a.zlabel = w.zlabel;
+        a.part = w.part;
         CUtensorMap tm[4];
         e = make_tma_16bit(&tm[0], d_x, T, dim, kBM, false);
         if (e == cudaSuccess) e = make_tma_16bit(&tm[1], d_head, vocab, dim, kBM, false);
@@ -534,7 +580,7 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
         e = launch_grad_lse(a, tm, s);
     }
     if (e == cudaSuccess)
-        e = launch_loss_combine(part, groups, T, zlabel, d_labels, (int)vocab, d_loss, d_lse, ctx->d_err, s);
+        e = launch_loss_combine(w.part, groups, T, w.zlabel, d_labels, (int)vocab, d_loss, d_lse, ctx->d_err, s);
     if (e != cudaSuccess) return cuda_fail(e, "loss launch");
     return ok();
 }

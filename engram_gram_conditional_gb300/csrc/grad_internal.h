@@ -136,6 +136,8 @@ struct EmbedSum {
     int lanes, slices;       // set by the launcher
 };
 int embed_rows_per_chunk(int64_t n, int dim, int copies);
+// Chunks of any number of copies and at most n ids.
+int64_t embed_most_chunks(int64_t n, int dim);
 cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s);
 
 // ---- gate (kernels_gate.cu) ----

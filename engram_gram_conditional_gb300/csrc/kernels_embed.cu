@@ -825,15 +825,37 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
     return cudaLaunchCooperativeKernel((void*)k_embed_sort, dim3(blocks), dim3(kSortThreads), args, smem, s);
 }
 
+// Chunks that fill the GPU four times over.
+static int64_t embed_chunks_wanted(int dim) {
+    const int64_t lanes = 1 << std::min(5, log2_ceil(dim / 8));
+    const int64_t slices = (dim / 8 + lanes - 1) / lanes;
+    return ((int64_t)device_sm_count() * 4 * 768 + slices * lanes - 1) / (slices * lanes);
+}
+
 // Sorted places per chunk: 64 rows of dout (a chunk's two partial rows are then
 // a few percent of what it reads), fewer while the chunks do not fill the GPU
 // four times over.
 int embed_rows_per_chunk(int64_t n, int dim, int copies) {
-    const int64_t lanes = 1 << std::min(5, log2_ceil(dim / 8));
-    const int64_t slices = (dim / 8 + lanes - 1) / lanes;
+    const int64_t want = embed_chunks_wanted(dim);
     int r = 64 / copies;
-    while (r > 4 && n / r * slices * lanes < (int64_t)device_sm_count() * 4 * 768) r /= 2;
+    while (r > 4 && n / r < want) r /= 2;
     return r;
+}
+
+// Where chunks of r places are too few, r is halved: so 2 r places make a chunk of
+// the most ids at which half as many chunks were still too few.
+int64_t embed_most_chunks(int64_t n, int dim) {
+    const int64_t want = embed_chunks_wanted(dim);
+    int64_t most = 0;
+    for (int copies = 1; copies <= 8; ++copies) {
+        int64_t upto = n;  // ids that chunks of r places take at most
+        for (int r = 64 / copies;; r /= 2) {
+            most = std::max(most, (upto + r - 1) / r);
+            if (r <= 4) break;
+            upto = std::min(upto, want * r - 1);
+        }
+    }
+    return most;
 }
 
 cudaError_t launch_embed_sum(EmbedSum a, int64_t n, cudaStream_t s) {

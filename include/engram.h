@@ -466,7 +466,9 @@ engram_status engram_gate_bf16kv(const engram_ctx* ctx, int layer, const uint16_
  * its 16-byte device word at its first engram_embed, engram_embed_grad,
  * engram_loss or engram_loss_backward: make that call before a stream capture.
  * Workspaces are device memory, 16-byte aligned, free again when the call's work
- * on the stream is done. */
+ * on the stream is done.  A workspace of the size given for n ids or T tokens
+ * holds for every smaller number too, so one of the largest batch's size does
+ * for all. */
 
 /* Embedding lookup with scaling: out[t][c] = scale table[ids[t]] for c < copies
  * (the hyper-connection branches start as copies of one embedding).
@@ -569,7 +571,7 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
  * summed in fp32 and rounded once.  d_lse: engram_loss's; d_dloss fp32 [T]; d_dx or d_dhead
  * may be NULL.  d_workspace: engram_loss_backward_workspace_bytes(T, vocab, dim)
  * bytes: the piece's dz (about 64 MB, 8 KB per token for a very long batch)
- * and the fp32 dx. */
+ * and the fp32 dx (one, or parts of it within 64 MB). */
 size_t engram_loss_backward_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim);
 engram_status engram_loss_backward(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
                                    uint32_t vocab, uint32_t dim, const int32_t* d_labels, int64_t T,

@@ -624,6 +624,73 @@ def test_loss_of_large_logits(plain_ctx):
     assert ((loss.cpu().to(F) - rloss).abs() <= 2 * tol).all()
 
 
+# ---- one workspace for every batch ------------------------------------------------------------
+
+def guarded(need):
+    """A workspace of `need` bytes between guards, and the test that they are whole."""
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    return ws[256:], lambda: bool((ws[:256] == 0xA5).all() and (ws[256 + need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("copies", [1, 3, 8])
+def test_embed_grad_of_smaller_batches_in_the_workspace_of_the_largest(plain_ctx, copies):
+    rows, dim = 900, 5120
+    most = 7300  # (three copies' rows: 3,644 ids make 1,822 chunks of two places, 3,700 make 740 of five)
+    ws, whole = guarded(eg.engram_embed_grad_workspace_bytes(most, rows, dim))
+    for n in (1, 700, 1867, 3500, 3644, 3700, most):
+        ids, dout = ids_like("zipf", n, rows, n).cuda(), rnd(n, n, 1, dim).cuda().expand(n, copies, dim).contiguous()
+        out = []
+        for w in (ws, ws_of(eg.engram_embed_grad_workspace_bytes(1 << 20, rows, dim))):
+            grad = torch.zeros(rows, dim, device="cuda")
+            eg.engram_embed_grad(plain_ctx, rows, dim, ids, n, 1.0, copies, dout, None, None, grad, 0, w)
+            out.append(grad)
+        eg.engram_sync(plain_ctx)
+        assert torch.equal(*out) and whole(), n
+
+
+@pytest.mark.parametrize("hc,d,heads,row_dim,sizes", [(4, 5120, 8, 256, (100, 256, 400, 1024, 1500)),
+                                                      (2, 1280, 4, 128, (64, 300, 1500, 3000))])
+def test_project_backward_of_smaller_batches_in_the_workspace_of_the_largest(hc, d, heads, row_dim, sizes):
+    N, K = (hc + 1) * d, 3 * heads * row_dim
+    s = make_layer(hc, d, heads, row_dim, wkv=rnd(1, N, K))
+    ws, whole = guarded(eg.engram_project_backward_workspace_bytes(s.ctx, sizes[-1]))
+    plenty = ws_of(1 << 28)
+    for T in sizes:
+        emb, dkv = rnd(T, T, K).cuda(), rnd(T + 1, T, N).cuda()
+        for want_dwkv in (True, False):
+            out = []
+            for w in (ws, plenty):
+                demb = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+                dwkv = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda") if want_dwkv else None
+                eg.engram_project_backward(s.ctx, 0, emb, dkv, T, demb, dwkv, w)
+                out.append(demb)
+            eg.engram_sync(s.ctx)
+            assert torch.equal(*out) and whole(), T
+    s.close()
+
+
+@pytest.mark.parametrize("V,dim,sizes", [(1000, 64, (1, 16, 17, 31)), (32_000, 2048, (16, 300, 1280, 1500))])
+def test_loss_of_smaller_batches_in_the_workspace_of_the_largest(plain_ctx, V, dim, sizes):
+    head = rnd(V, V, dim, sigma=2 / math.sqrt(dim)).cuda()
+    ws, whole = guarded(eg.engram_loss_workspace_bytes(sizes[-1], V, dim))
+    back, back_whole = guarded(eg.engram_loss_backward_workspace_bytes(sizes[-1], V, dim))
+    plenty = ws_of(1 << 28)
+    for T in sizes:
+        x, _, y = loss_problem(T, 2, dim)
+        x, y, dloss = x.cuda(), y.cuda(), torch.ones(T, device="cuda")
+        out = []
+        for w, wb in ((ws, back), (plenty, plenty)):
+            loss, lse = (torch.zeros(T, device="cuda") for _ in range(2))
+            dx, dhead = torch.zeros_like(x), torch.zeros_like(head)
+            eg.engram_loss(plain_ctx, x, head, V, dim, y, T, loss, lse, w)
+            eg.engram_loss_backward(plain_ctx, x, head, V, dim, y, T, lse, dloss, dx, dhead, wb)
+            only = torch.zeros_like(x)
+            eg.engram_loss_backward(plain_ctx, x, head, V, dim, y, T, lse, dloss, only, None, wb)
+            out.append((loss, lse, dx, dhead, only))
+        eg.engram_sync(plain_ctx)
+        assert all(torch.equal(a, b) for a, b in zip(*out)) and whole() and back_whole(), T
+
+
 # ---- streams ---------------------------------------------------------------------------------------
 
 def test_operators_run_on_their_own_stream(plain_ctx):

@@ -91,3 +91,31 @@ def test_workspace_sizes(ctx):
     # no logits: the loss keeps two floats per 128 columns, the backward pass one piece
     assert eg.engram_loss_workspace_bytes(2048, 129_280, 5120) < 2048 * 129_280 // 8
     assert eg.engram_loss_backward_workspace_bytes(2048, 129_280, 5120) < 2048 * 129_280 * 2 // 4
+
+
+def geometry(hc, d, heads, row_dim):
+    return eg.engram_ctx_create(64, 60, np.arange(64, dtype=np.uint32) % 60, [3], [50], heads=heads,
+                                row_dim=row_dim, hc=hc, d=d)
+
+
+SIZES = sorted({*range(1, 700), *range(700, 20_000, 61), *(2 ** k + e for k in range(9, 18) for e in (-1, 0, 1))})
+
+
+@pytest.mark.parametrize("of", ["embed_grad", "gate_backward", "project_backward", "loss", "loss_backward"])
+def test_a_workspace_holds_for_every_smaller_batch(of):
+    """Sizes never fall as the batch grows."""
+    def check(f):
+        sizes = [f(n) for n in SIZES]
+        assert sizes == sorted(sizes)
+
+    if of == "embed_grad":
+        for rows, dim in ((129_280, 5120), (64_000_000, 256), (5000, 40), (100, 8), (70_000, 65_536)):
+            check(lambda n: eg.engram_embed_grad_workspace_bytes(n, rows, dim))
+    elif of in ("loss", "loss_backward"):
+        for vocab, dim in ((1000, 64), (31, 1032), (32_000, 2048), (129_280, 5120), (129_280, 8)):
+            check(lambda n: getattr(eg, f"engram_{of}_workspace_bytes")(n, vocab, dim))
+    else:
+        for g in ((4, 5120, 8, 256), (1, 256, 2, 32), (2, 1280, 4, 128), (8, 2560, 3, 64)):
+            c = geometry(*g)
+            check(lambda n: getattr(eg, f"engram_{of}_workspace_bytes")(c, n))
+            eg.engram_ctx_destroy(c)
