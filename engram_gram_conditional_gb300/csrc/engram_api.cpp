@@ -890,8 +890,20 @@ engram_status engram_batch_append(engram_session* const* sessions, const int32_t
 // ---- device steps ---------------------------------------------------------------------
 
 
+// The most that f needs for any batch of at most T tokens.  f grows with T but for
+// the parts that only batches whose output tiles do not fill the GPU twice need
+// (parked tiles), and among those within a 128-token block: so T itself and the
+// last batch of each such block are all there is to look at.
+static size_t most_up_to(const engram_ctx* ctx, int64_t T, size_t (*f)(const engram_ctx*, int64_t)) {
+    size_t most = f(ctx, T);
+    const int64_t nt = ctx->N / kBN, few = 2 * (int64_t)device_sm_count();
+    for (int64_t t = kBM; t < T && t / kBM * nt < few; t += kBM) most = std::max(most, f(ctx, t));
+    return most;
+}
+
 size_t engram_workspace_bytes(const engram_ctx* ctx, int64_t T) {
-    return forward_workspace_bytes(ctx, T, 8);
+    if (!ctx || T <= 0) return 0;
+    return most_up_to(ctx, T, [](const engram_ctx* c, int64_t t) { return forward_workspace_bytes(c, t, 8); });
 }
 
 static engram_status hash_impl(const engram_ctx* ctx, int layer, const uint32_t* d_windows,
@@ -1039,14 +1051,19 @@ static size_t staged_e_bytes(const engram_ctx* ctx, int64_t T) {
     return (rows * ctx->K * sizeof(uint16_t) + 255) & ~(size_t)255;
 }
 
-size_t engram_forward_staged_workspace_bytes(const engram_ctx* ctx, int64_t T) {
-    if (!ctx || T <= 0) return 0;
+static size_t staged_need(const engram_ctx* ctx, int64_t T) {
     const size_t e = staged_e_bytes(ctx, T);
     if (staged_stream_k(ctx, T)) return e + stream_k_ws(ctx, T).total();
     // the TMA-fed kernels run two epilogue warps per TMEM quadrant; then one
     // has-text flag per 128-token block
     return e + forward_workspace_bytes_groups(ctx, T, 8, 2) +
            ((((size_t)T + kBM - 1) / kBM * sizeof(uint32_t) + 255) & ~(size_t)255);
+}
+
+// (A long batch's chunks are smaller batches on the same workspace.)
+size_t engram_forward_staged_workspace_bytes(const engram_ctx* ctx, int64_t T) {
+    if (!ctx || T <= 0) return 0;
+    return most_up_to(ctx, T, staged_need);
 }
 
 // The has-text flags of a large batch's blocks in its staged workspace (null

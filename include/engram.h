@@ -235,8 +235,10 @@ engram_status engram_batch_append(engram_session* const* sessions, const int32_t
  * 128 tokens x 256 outputs per SM) is run with K split over up to 8 CTAs per
  * tile, and the workspace then also holds the parked fp32 partial tiles:
  * 128 KB per (128-token block, 256-output tile, split), e.g. 79 MB for 256
- * tokens at N = 25,600.  Ask again after switching to a device with another
- * SM count. */
+ * tokens at N = 25,600.  A workspace of the size given for T tokens holds for
+ * every smaller batch too (so does that of
+ * engram_forward_staged_workspace_bytes).  Ask again after switching to a
+ * device with another SM count. */
 size_t engram_workspace_bytes(const engram_ctx* ctx, int64_t T);
 
 /* The n-gram hash.  "DeepSeek V4.1 Flash 的 Engram", section "第一步": the

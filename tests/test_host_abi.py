@@ -238,6 +238,18 @@ def test_device_calls_validate_before_launch():
     eg.engram_ctx_destroy(ctx)
 
 
+@pytest.mark.parametrize("geometry", [dict(), dict(hc=4, d=5120, heads=8, row_dim=256),
+                                      dict(hc=1, d=256, heads=8, row_dim=256), dict(hc=8, d=2560)])
+def test_a_workspace_holds_for_every_smaller_batch(geometry):
+    """Sizes never fall as the batch grows: a long batch's chunks and a smaller batch run on it."""
+    ctx, _ = tiny_ctx(**geometry)
+    sizes = sorted({*range(1, 1100), *range(1100, 60_000, 127)})
+    for f in (eg.engram_workspace_bytes, eg.engram_forward_staged_workspace_bytes):
+        got = [f(ctx, T) for T in sizes]
+        assert got == sorted(got)
+    eg.engram_ctx_destroy(ctx)
+
+
 def test_last_error_is_set_and_cleared():
     ctx, _ = tiny_ctx()
     with pytest.raises(eg.EngramError):
