@@ -38,15 +38,23 @@ class TrainStep:
 
     ``model``: an EngramLayerSet with ``layer`` bound; ``embedding`` and ``head``:
     BF16 [vocab][d].  ``kv_format``: how kv waits for the gate (KV_F32 or KV_BF16).
+
+    A step's number of tokens T is that of the ids which forward() is given; what
+    the buffers hold past T tokens is left over from longer steps.
     """
 
     def __init__(self, model, layer: int, embedding, head, tokens: int, *, kv_format=KV_BF16,
                  scale=None):
         g = model.geom
+        if tokens < 1:
+            raise ValueError("tokens must be at least 1")
+        for name, w in (("embedding", embedding), ("head", head)):
+            self._check(name, w, 2, (embedding.shape[0], g["d"]), model.device)
         self.model, self.layer, self.embedding, self.head = model, layer, embedding, head
         self.vocab, self.d, self.hc = embedding.shape[0], g["d"], g["hc"]
         self.kv_format, self.scale = kv_format, math.sqrt(g["d"]) if scale is None else scale
         self.tokens = tokens
+        self.T = 0  # tokens of the last forward()
         T, nb, K, N, kept = tokens, model.nb, model.K, model.N, (2 * self.hc + 1) * self.d
         bf16, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
@@ -77,10 +85,28 @@ class TrainStep:
                           engram_embed_grad_workspace_bytes(T * nb, model.rows(layer),
                                                             g["row_dim"]), 16), dtype=u8)
 
+    @staticmethod
+    def _check(name, x, size, shape, device):
+        """The kernels read as far as the shapes say: a tensor of another number of values, or of
+        values that do not have `size` bytes, is refused."""
+        if x.element_size() != size or x.numel() != math.prod(shape) or not x.is_contiguous():
+            raise ValueError(f"{name}: {list(shape)} of {size} bytes each, contiguous, expected; "
+                             f"got {x.dtype} {list(x.shape)}")
+        if x.device.type != device.type or (device.index is not None and x.device.index != device.index):
+            raise ValueError(f"{name}: on {x.device}, the model is on {device}")
+
+    def _check_step(self, ids, windows, labels, T):
+        for name, x, shape in (("ids", ids, (T,)), ("windows", windows, (T, 4)), ("labels", labels, (T,))):
+            self._check(name, x, 4, shape, self.model.device)
+
     def forward(self, ids, windows, labels, stream=None):
         """Loss of each token (fp32 [T]); ids and labels int32 [T], windows int32 [T][4] (an
-        image row has slot 0 DEAD), all on the device."""
-        ctx, layer, T = self.model.ctx, self.layer, self.tokens
+        image row has slot 0 DEAD), all on the device, T at most ``tokens``."""
+        ctx, layer, T = self.model.ctx, self.layer, ids.numel()
+        if not 0 < T <= self.tokens:
+            raise ValueError(f"{T} tokens: 1 to {self.tokens} are possible")
+        self._check_step(ids, windows, labels, T)
+        self.T = T
         engram_embed(ctx, self.embedding, EMBED_BF16, self.vocab, self.d, ids, T, self.scale, self.hc,
                      self.hidden, stream)
         engram_hash(ctx, layer, windows, T, self.rows, stream)
@@ -88,18 +114,23 @@ class TrainStep:
         engram_prepass(ctx, layer, windows, T, self.kv, self.kv_format, self.ws, stream)
         engram_gate_checkpoint(ctx, layer, self.kv, self.kv_format, windows, T, self.hidden, self.out,
                                self.gates, self.codes, self.scales, stream)
-        self.x = self.out.float().mean(1).bfloat16()
+        self.x = self.out[:T].float().mean(1).bfloat16()
         engram_loss(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.loss, self.lse, self.ws,
                     stream)
-        return self.loss
+        return self.loss[:T]
 
     def backward(self, ids, windows, labels, dloss, stream=None):
         """Gradients of sum(dloss * loss) (dloss fp32 [T]) into this object's buffers: dhead, dwq,
-        dwk, dwkv, and the sparse token_ids/token_grad and row_ids/row_grad with their counts."""
-        ctx, layer, T = self.model.ctx, self.layer, self.tokens
+        dwk, dwkv, and the sparse token_ids/token_grad and row_ids/row_grad with their counts.
+        ids, windows and labels are those of the forward() before."""
+        ctx, layer, T = self.model.ctx, self.layer, self.T
+        if T == 0:
+            raise ValueError("no forward() to go back through")
+        self._check_step(ids, windows, labels, T)
+        self._check("dloss", dloss, 4, (T,), self.model.device)
         engram_loss_backward(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.lse, dloss,
                              self.dx, self.dhead, self.ws, stream)
-        dout = (self.dx.float() / self.hc).bfloat16().unsqueeze(1).expand(-1, self.hc, -1).contiguous()
+        dout = (self.dx[:T].float() / self.hc).bfloat16().unsqueeze(1).expand(-1, self.hc, -1).contiguous()
         engram_gate_backward_checkpoint(ctx, layer, self.codes, self.scales, windows, T, dout,
                                         self.dhidden, self.dkv, self.dwq, self.dwk, self.ws, stream)
         engram_project_backward(ctx, layer, self.emb, self.dkv, T, self.demb, self.dwkv, self.ws, stream)

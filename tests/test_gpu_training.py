@@ -21,6 +21,7 @@ import torch
 
 import engram_gram_conditional_gb300 as eg
 from engram_gram_conditional_gb300.layer import EngramLayerSet
+from engram_gram_conditional_gb300.training import TrainStep
 
 pytestmark = pytest.mark.gpu
 F = torch.float64
@@ -818,6 +819,65 @@ def test_operators_in_a_captured_graph(plain_ctx):
         torch.cuda.synchronize()
         for a, b in zip(got, (grad, loss, lse, dx, dhead)):
             assert torch.equal(a, b)
+
+
+# ---- the step -----------------------------------------------------------------------------------
+
+VOCAB, D = 500, 256
+
+
+def step_model(hc=2, seed=0):
+    """A small model around one layer with a BF16 table, as the example's."""
+    s = EngramLayerSet(VOCAB, 400, np.arange(VOCAB, dtype=np.uint32) % 400, [3], [200], heads=2,
+                       row_dim=32, hc=hc, d=D)
+    g = torch.Generator().manual_seed(seed)
+    new = lambda *shape, sigma=1.0: torch.randn(*shape, generator=g) * sigma  # noqa: E731
+    kept = s.bind(0, 11, new((hc + 1) * D, 192, sigma=192 ** -0.5).bfloat16().cuda().view(torch.int16),
+                  1 + new(hc, D, sigma=0.1), 1 + new(hc, D, sigma=0.1), flags=eg.BIND_TABLE_BF16)
+    embedding, head = new(VOCAB, D, sigma=D ** -0.5), new(VOCAB, D, sigma=2 * D ** -0.5)
+    return s, kept, embedding.bfloat16().cuda(), head.bfloat16().cuda()
+
+
+def step_inputs(s, T, seed):
+    tokens = np.random.default_rng(seed).integers(0, VOCAB, T + 1).astype(np.int32)
+    session = eg.engram_session_create(s.ctx)
+    image = np.zeros(T, np.uint8)
+    image[T // 3] = 1
+    windows = eg.engram_session_append(session, tokens[:-1], image)
+    eg.engram_session_destroy(session)
+    labels = tokens[1:].copy()
+    labels[T // 2] = -1
+    dloss = rnd(seed, T, dtype=torch.float32).abs() + 0.5
+    return [torch.from_numpy(a).cuda() for a in (tokens[:-1].copy(), windows.view(np.int32), labels)] + [dloss.cuda()]
+
+
+def step_outputs(step, loss):
+    n, r = int(step.token_count), int(step.row_count)
+    return [loss.clone(), step.dhead.clone(), step.dwq.clone(), step.dwk.clone(), step.dwkv.clone(),
+            step.token_ids[:n].clone(), step.token_grad[:n].clone(), step.row_ids[:r].clone(),
+            step.row_grad[:r].clone()]
+
+
+def run_step(step, inputs, stream=None):
+    loss = step.forward(*inputs[:3], stream)
+    step.backward(*inputs, stream)
+    return loss
+
+
+def test_a_step_of_fewer_tokens_is_that_of_buffers_of_their_size():
+    s, _, embedding, head = step_model()
+    big = TrainStep(s, 0, embedding, head, 300)
+    run_step(big, step_inputs(s, 300, 1))  # what the buffers hold past a shorter step
+    for T in (1, 2, 16, 17, 129, 299, 300):
+        inputs = step_inputs(s, T, T)
+        loss = run_step(big, inputs)
+        own = TrainStep(s, 0, embedding, head, T)
+        own_loss = run_step(own, inputs)
+        eg.engram_sync(s.ctx)
+        assert loss.shape == (T,)
+        for a, b in zip(step_outputs(big, loss), step_outputs(own, own_loss)):
+            assert torch.equal(a, b), T
+    s.close()
 
 
 def test_training_example_learns():

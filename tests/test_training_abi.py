@@ -1,8 +1,12 @@
 """Refusals of the training operators (no GPU): arguments are checked before any launch."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
+import torch
 
 import engram_gram_conditional_gb300 as eg
+from engram_gram_conditional_gb300.training import TrainStep
 
 
 @pytest.fixture(scope="module")
@@ -119,3 +123,41 @@ def test_a_workspace_holds_for_every_smaller_batch(of):
             c = geometry(*g)
             check(lambda n: getattr(eg, f"engram_{of}_workspace_bytes")(c, n))
             eg.engram_ctx_destroy(c)
+
+
+def tensors(**bad):
+    t = dict(ids=torch.zeros(5, dtype=torch.int32), windows=torch.zeros(5, 4, dtype=torch.int32),
+             labels=torch.zeros(5, dtype=torch.int32), dloss=torch.zeros(5))
+    return {**t, **bad}
+
+
+@pytest.mark.parametrize("bad", [dict(ids=torch.zeros(0, dtype=torch.int32)), dict(ids=torch.zeros(9, dtype=torch.int32)),
+                                 dict(ids=torch.zeros(5, dtype=torch.int64)),
+                                 dict(windows=torch.zeros(4, 4, dtype=torch.int32)),
+                                 dict(windows=torch.zeros(4, 5, dtype=torch.int32).t()),
+                                 dict(labels=torch.zeros(4, dtype=torch.int32)),
+                                 dict(labels=torch.zeros(5, dtype=torch.int64)),
+                                 dict(labels=torch.zeros(10, dtype=torch.int32)[::2]),
+                                 dict(labels=torch.zeros(5, dtype=torch.int32, device="meta"))])
+def test_a_step_refuses_tensors_that_do_not_go_together(bad):
+    step = object.__new__(TrainStep)  # (its buffers need a GPU; what is refused reaches none)
+    step.model, step.layer, step.tokens, step.T = SimpleNamespace(device=torch.device("cpu"), ctx=None), 0, 8, 0
+    t = tensors(**bad)
+    with pytest.raises(ValueError):
+        step.forward(t["ids"], t["windows"], t["labels"])
+    assert step.T == 0
+    with pytest.raises(ValueError):
+        step.backward(*tensors().values())  # no forward before
+    step.T = 5
+    t = tensors(**bad) if "ids" not in bad or bad["ids"].numel() else tensors(dloss=torch.zeros(4))
+    with pytest.raises(ValueError):
+        step.backward(*t.values())
+
+
+def test_a_step_refuses_weights_of_another_shape():
+    model = SimpleNamespace(device=torch.device("cpu"), geom=dict(d=256, hc=2, row_dim=32), ctx=None)
+    good = torch.zeros(10, 256, dtype=torch.bfloat16)
+    for embedding, head, tokens in ((good, good[:9], 4), (good, good.float(), 4), (good[:, :128], good, 4),
+                                    (good, good.t(), 4), (good, good, 0)):
+        with pytest.raises(ValueError):
+            TrainStep(model, 0, embedding, head, tokens)
