@@ -41,6 +41,9 @@ class TrainStep:
 
     A step's number of tokens T is that of the ids which forward() is given; what
     the buffers hold past T tokens is left over from longer steps.
+
+    ``stream`` of a call: a torch stream or a handle; None is torch's current one.
+    All of a step, the library's calls and torch's alike, runs on it.
     """
 
     def __init__(self, model, layer: int, embedding, head, tokens: int, *, kv_format=KV_BF16,
@@ -67,7 +70,7 @@ class TrainStep:
         self.gates = new(T, self.hc, dtype=f32)
         self.codes, self.scales = new(T, kept, dtype=u8), new(T, kept // 32, dtype=u8)
         self.loss, self.lse = new(T, dtype=f32), new(T, dtype=f32)
-        self.dx, self.dhead = new(T, self.d), new(self.vocab, self.d)
+        self.x, self.dx, self.dhead = new(T, self.d), new(T, self.d), new(self.vocab, self.d)
         self.dhidden, self.dkv = new(T, self.hc, self.d), new(T, N)
         self.dwq, self.dwk = new(self.hc, self.d, dtype=f32), new(self.hc, self.d, dtype=f32)
         self.demb, self.dwkv = new(T, K), new(N, K)
@@ -84,6 +87,16 @@ class TrainStep:
                           engram_embed_grad_workspace_bytes(T, self.vocab, self.d),
                           engram_embed_grad_workspace_bytes(T * nb, model.rows(layer),
                                                             g["row_dim"]), 16), dtype=u8)
+        # a step may run on another stream than the one whose freed memory this is
+        torch.cuda.current_stream(model.device).synchronize()
+
+    def _on(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.model.device)
+        if isinstance(stream, int):
+            return (torch.cuda.ExternalStream(stream, self.model.device) if stream else
+                    torch.cuda.default_stream(self.model.device))
+        return stream
 
     @staticmethod
     def _check(name, x, size, shape, device):
@@ -106,7 +119,7 @@ class TrainStep:
         if not 0 < T <= self.tokens:
             raise ValueError(f"{T} tokens: 1 to {self.tokens} are possible")
         self._check_step(ids, windows, labels, T)
-        self.T = T
+        self.T, stream = T, self._on(stream)
         engram_embed(ctx, self.embedding, EMBED_BF16, self.vocab, self.d, ids, T, self.scale, self.hc,
                      self.hidden, stream)
         engram_hash(ctx, layer, windows, T, self.rows, stream)
@@ -114,7 +127,8 @@ class TrainStep:
         engram_prepass(ctx, layer, windows, T, self.kv, self.kv_format, self.ws, stream)
         engram_gate_checkpoint(ctx, layer, self.kv, self.kv_format, windows, T, self.hidden, self.out,
                                self.gates, self.codes, self.scales, stream)
-        self.x = self.out[:T].float().mean(1).bfloat16()
+        with torch.cuda.stream(stream):
+            self.x[:T] = self.out[:T].float().mean(1)
         engram_loss(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.loss, self.lse, self.ws,
                     stream)
         return self.loss[:T]
@@ -128,10 +142,12 @@ class TrainStep:
             raise ValueError("no forward() to go back through")
         self._check_step(ids, windows, labels, T)
         self._check("dloss", dloss, 4, (T,), self.model.device)
+        stream = self._on(stream)
         engram_loss_backward(ctx, self.x, self.head, self.vocab, self.d, labels, T, self.lse, dloss,
                              self.dx, self.dhead, self.ws, stream)
-        dout = (self.dx[:T].float() / self.hc).bfloat16().unsqueeze(1).expand(-1, self.hc, -1).contiguous()
-        engram_gate_backward_checkpoint(ctx, layer, self.codes, self.scales, windows, T, dout,
+        with torch.cuda.stream(stream):  # the mean's gradient; the gate's call replaces it in place
+            self.dhidden[:T] = (self.dx[:T].float() / self.hc).unsqueeze(1)
+        engram_gate_backward_checkpoint(ctx, layer, self.codes, self.scales, windows, T, self.dhidden,
                                         self.dhidden, self.dkv, self.dwq, self.dwk, self.ws, stream)
         engram_project_backward(ctx, layer, self.emb, self.dkv, T, self.demb, self.dwkv, self.ws, stream)
         engram_embed_grad(ctx, self.vocab, self.d, ids, T, self.scale, self.hc, self.dhidden,

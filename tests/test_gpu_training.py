@@ -880,6 +880,40 @@ def test_a_step_of_fewer_tokens_is_that_of_buffers_of_their_size():
     s.close()
 
 
+@pytest.mark.parametrize("given", ["none", "stream", "handle"])
+def test_a_step_runs_on_its_stream(given):
+    """All of a step is on one stream: the current one where none is given, else the given one,
+    whatever the current one is.  The stream's work before it (a wait of some ten milliseconds,
+    then the copy of the inputs) is done first, and nothing of the step runs before that."""
+    T = 120
+    s, _, embedding, head = step_model()
+    inputs = step_inputs(s, T, 5)
+    step = TrainStep(s, 0, embedding, head, T)
+    loss = run_step(step, inputs)
+    eg.engram_sync(s.ctx)
+    want = step_outputs(step, loss)
+    step = TrainStep(s, 0, embedding, head, T)
+    for x in vars(step).values():  # what a step that runs too early would find
+        if isinstance(x, torch.Tensor) and x is not embedding and x is not head:
+            x.zero_()
+    late = [torch.zeros_like(x) for x in inputs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        for a, b in zip(late, inputs):
+            a.copy_(b)
+    if given == "none":
+        with torch.cuda.stream(side):
+            loss = run_step(step, late)
+    else:
+        loss = run_step(step, late, side if given == "stream" else side.cuda_stream)
+    eg.engram_sync(s.ctx, side)
+    for a, b in zip(step_outputs(step, loss), want):
+        assert torch.equal(a, b)
+    s.close()
+
+
 def test_training_example_learns():
     import importlib.util
     import os
