@@ -14,6 +14,7 @@
 #include <algorithm>
 
 #include "grad_internal.h"
+#include "per_device.h"
 #include "tcgen05_common.cuh"
 #include "train_common.cuh"
 
@@ -790,12 +791,16 @@ void embed_sort_digits(uint64_t rows, int* passes, int* bits) {
     *bits = (need + *passes - 1) / *passes;
 }
 
+// Shared memory for digits of `bits` bits and `keys` pairs.
+static int embed_sort_smem(int bits, int keys) { return kSortWarps * (1 << bits) * 4 + keys * 8; }
+
 cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
     if (a.n <= kSmallSort) {
-        const int per = a.n <= kSortThreads * 8 ? 1 : a.n <= kSortThreads * 16 ? 2 : 4;
+        static PerDevice allowed[3];
+        const int size = a.n <= kSortThreads * 8 ? 0 : a.n <= kSortThreads * 16 ? 1 : 2, per = 1 << size;
         auto f = per == 1 ? k_embed_sort_small<1> : per == 2 ? k_embed_sort_small<2> : k_embed_sort_small<4>;
-        const int smem = kSortWarps * (1 << a.digit_bits) * 4 + 2 * kSortThreads * per * 8;
-        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const int keys = 2 * kSortThreads * per, smem = embed_sort_smem(a.digit_bits, keys);
+        const cudaError_t e = allow_shared(allowed[size], f, embed_sort_smem(9, keys));
         if (e != cudaSuccess) return e;
         unsigned cs = 1;
         while (cs * kSortThreads * per < a.n) cs *= 2;
@@ -816,8 +821,9 @@ cudaError_t launch_embed_sort(const EmbedSort& a, cudaStream_t s) {
         return cudaLaunchKernelEx(&cfg, f, a);
     }
     const int blocks = embed_sort_blocks(a.n);
-    const int smem = kSortWarps * (1 << a.digit_bits) * 4 + kSortThreads * kSortBatch * 8;
-    cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static PerDevice allowed;
+    const int keys = kSortThreads * kSortBatch, smem = embed_sort_smem(a.digit_bits, keys);
+    cudaError_t e = allow_shared(allowed, k_embed_sort, embed_sort_smem(9, keys));
     if (e == cudaSuccess) e = cudaMemsetAsync(a.barrier, 0, 8, s);  // with *a.failed
     if (e != cudaSuccess) return e;
     EmbedSort copy = a;

@@ -21,6 +21,7 @@
 
 #include "device_common.cuh"
 #include "grad_internal.h"
+#include "per_device.h"
 #include "tcgen05_common.cuh"
 
 namespace engram {
@@ -284,8 +285,8 @@ cudaError_t launch(const FewArgs& a, const uint16_t* x, const uint16_t* head, in
     if (e == cudaSuccess) e = make_tma_16bit(&tmU, head, head_rows, dim, kUnit, false);
     if (e == cudaSuccess) e = make_tma_16bit(&tmX, x, a.T, dim, kN, false);
     auto kern = k_few<kDz>;
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kSmem);
+    static PerDevice allowed;
+    if (e == cudaSuccess) e = allow_shared(allowed, kern, Layout::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

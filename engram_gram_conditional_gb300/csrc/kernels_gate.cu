@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "grad_internal.h"
+#include "per_device.h"
 #include "tcgen05_common.cuh"
 #include "train_common.cuh"
 
@@ -993,9 +994,11 @@ cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_by
                             cudaStream_t s) {
     const int per = (a.d / 256 + cs - 1) / cs;
     const int smem = (kFusedFixed + 127) / 128 * 128 + stages * stage_bytes;
-    static const cudaError_t allowed =
-        cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (allowed != cudaSuccess) return allowed;
+    static PerDevice allowed;
+    int dev = 0;
+    cudaError_t e = allow_shared(allowed, kKernel, 227 * 1024);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1005,22 +1008,21 @@ cudaError_t one_pass_launch(const GateTrain& a, int cs, int stages, int stage_by
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     // as many clusters as are resident at once (larger ones leave SMs of a GPC over),
-    // asked for when the shape changes, and no more than `most`
-    static thread_local struct { int cs, per, smem, clusters; } known = {};
+    // asked for when the shape or the device changes, and no more than `most`
+    static thread_local struct { int dev, cs, per, smem, clusters; } known = {};
     cfg.gridDim = dim3(device_sm_count() / cs * cs);
     cfg.blockDim = dim3((per + 2) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr + 1;
     cfg.numAttrs = 1;
-    if (known.cs != cs || known.per != per || known.smem != smem) {
+    if (known.dev != dev || known.cs != cs || known.per != per || known.smem != smem) {
         int resident = 1;
-        const cudaError_t e =
-            cs > 1 ? cudaOccupancyMaxActiveClusters(&resident, kKernel, &cfg)
+        e = cs > 1 ? cudaOccupancyMaxActiveClusters(&resident, kKernel, &cfg)
                    : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kKernel, (per + 2) * 32, smem);
         if (e != cudaSuccess) return e;
         if (cs == 1) resident *= device_sm_count();
-        known = {cs, per, smem, std::max(1, resident)};
+        known = {dev, cs, per, smem, std::max(1, resident)};
     }
     *clusters = (int)std::min<int64_t>(a.T, std::min(known.clusters, most));
     cfg.gridDim = dim3(*clusters * cs);

@@ -33,6 +33,7 @@
 
 #include "device_common.cuh"
 #include "grad_internal.h"
+#include "per_device.h"
 #include "tcgen05_common.cuh"
 
 namespace engram {
@@ -741,11 +742,10 @@ cudaError_t pdl_launch(void* f, dim3 grid, dim3 block, void** args, cudaStream_t
 // dealt out for pairs that all run from the start.
 template <int kEpi>
 cudaError_t resident_pairs(int* pairs) {
-    static int known = 0;
-    if (!known) {
+    static PerDevice known, allowed;
+    return known.get(pairs, [](int* found) {
         auto kern = k_grad<kEpi>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Layout<kEpi>::kSmem);
+        cudaError_t e = allow_shared(allowed, kern, Layout<kEpi>::kSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -762,10 +762,9 @@ cudaError_t resident_pairs(int* pairs) {
         e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorLaunchOutOfResources;
-        known = std::min(n, device_sm_count() / 2);
-    }
-    *pairs = known;
-    return cudaSuccess;
+        *found = std::min(n, device_sm_count() / 2);
+        return cudaSuccess;
+    });
 }
 
 template <int kEpi>

@@ -6,25 +6,22 @@
 #include <algorithm>
 
 #include "device_common.cuh"
+#include "per_device.h"
 
 namespace engram {
 
 namespace {
 
-int g_sm_count = 0;
-
-// SMs of the current device (of the first one asked about); 152, a GB300's
-// count, when no device answers.
+// SMs of the current device; 152, a GB300's count, when no device answers.
 int sm_count() {
-    if (g_sm_count == 0) {
-        int dev = 0, n = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess &&
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-            g_sm_count = n;
-        else
-            return 152;
-    }
-    return g_sm_count;
+    static PerDevice known;
+    int n = 0;
+    const cudaError_t e = known.get(&n, [](int* sms) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    });
+    return e == cudaSuccess && n > 0 ? n : 152;
 }
 
 int grid_for(int64_t items, int threads, int per_sm) {

@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "device_common.cuh"
+#include "per_device.h"
 #include "tcgen05_common.cuh"
 
 namespace engram {
@@ -1503,14 +1504,10 @@ std::once_flag g_encode_once;
 template <int kASrc, bool kF16, int kMode>
 cudaError_t launch(const MmaArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB,
                    cudaStream_t s) {
-    static bool attr_set = false;
+    static PerDevice allowed;
     auto kern = k_mma<kASrc, kF16, kMode>;
     constexpr int kSmem = Layout<kASrc, k_blocks_per_stage<kASrc, kF16>(), kMode>::kBytes;
-    if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    if (const cudaError_t e = allow_shared(allowed, kern, kSmem); e != cudaSuccess) return e;
     // work units: the (tile, split)s, or with stream K the (tile, stage)s
     constexpr int kKS = k_blocks_per_stage<kASrc, kF16>();
     // stream K: the kv-store epilogue, or the gate-sum epilogue of kEpiForwardSk
