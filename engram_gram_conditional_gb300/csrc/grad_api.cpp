@@ -408,8 +408,8 @@ engram_status engram_gate_checkpoint(const engram_ctx* ctx, int layer, const voi
     if (T == 0) return ok();
     if (!d_kv || !d_windows || !d_hidden || !d_hidden_out || !d_codes || !d_scales ||
         !aligned16(d_kv) || !aligned16(d_windows) || !aligned16(d_hidden) ||
-        !aligned16(d_hidden_out) || !aligned16(d_codes) || !aligned16(d_scales))
-        return fail(ENGRAM_EINVAL, "kv / windows / hidden / codes / scales (16-byte aligned)");
+        !aligned16(d_hidden_out) || !aligned4(d_gates) || !aligned16(d_codes) || !aligned16(d_scales))
+        return fail(ENGRAM_EINVAL, "kv / windows / hidden / codes / scales (16-byte aligned) / gates");
     GateTrain a = gate_args(ctx, layer, d_windows, T);
     a.kv = d_kv;
     a.hidden = d_hidden;

@@ -298,6 +298,29 @@ def test_gate_checkpoint_of_many_and_of_wide_tokens(T, hc, d, kv_format):
     test_gate_checkpoint(T, hc, d, kv_format)
 
 
+def test_gate_calls_refuse_misaligned_pointers():
+    s = make_layer()
+    A = 1 << 20  # an aligned address that no refused call touches
+    good = dict(kv=A, windows=A, hidden=A, out=A, gates=A, codes=A, scales=A)
+    for name in good:
+        a = {**good, name: A + 2}
+        with pytest.raises(eg.EngramError) as e:
+            eg.engram_gate_checkpoint(s.ctx, 0, a["kv"], eg.KV_F32, a["windows"], 1, a["hidden"], a["out"],
+                                      a["gates"], a["codes"], a["scales"])
+        assert e.value.status == eg.EINVAL
+    names = ("windows", "dout", "dhidden", "dkv", "dwq", "dwk", "ws")
+    good = dict.fromkeys(("first", "second") + names, A)
+    for name in good:
+        a = {**good, name: A + 8}
+        last = (a["windows"], 1, a["dout"], a["dhidden"], a["dkv"], a["dwq"], a["dwk"], a["ws"])
+        for f, args in ((eg.engram_gate_backward, (a["first"], eg.KV_BF16, a["second"])),
+                        (eg.engram_gate_backward_checkpoint, (a["first"], a["second"]))):
+            with pytest.raises(eg.EngramError) as e:
+                f(s.ctx, 0, *args, *last)
+            assert e.value.status == eg.EINVAL
+    s.close()
+
+
 def test_gate_checkpoint_of_infinities_and_nans():
     T, hc, d = 1, 1, 256
     h, kv, win, wq, wk = gate_problem(T, hc, d, 5, image=())
