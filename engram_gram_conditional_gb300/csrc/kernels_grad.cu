@@ -111,12 +111,13 @@ __device__ __forceinline__ void put_box(uint32_t box, int lane, uint16_t* dst, i
     for (int k = 0; k < 8; ++k)
         if (4 * k + r0 < n) *reinterpret_cast<uint4*>(dst + 4 * k * ld) = v[k];
 }
-// Arrival on a barrier of the pair's even CTA that hands an accumulator back.  A
-// release at CTA scope: what it orders is this warp's reads of tensor memory,
-// which tcgen05.wait::ld has completed.  At cluster scope it would wait for the
-// warp's stores of the tile before (850 to 2,200 cycles per tile).
+// Arrival on a barrier of the pair's even CTA that hands an accumulator back.
+// Relaxed: what has to come before it are this warp's reads of tensor memory, which
+// tcgen05.wait::ld has completed and the tcgen05 fence orders.  A release at cluster
+// scope would wait for the warp's stores of the tile before (850 to 2,200 cycles per
+// tile).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // 32 bytes at a time: a whole sector per thread.
 __device__ __forceinline__ void ld_global_v8(const float* p, float (&f)[8]) {
