@@ -22,6 +22,7 @@ import torch
 import engram_gram_conditional_gb300 as eg
 from engram_gram_conditional_gb300.layer import EngramLayerSet
 from engram_gram_conditional_gb300.training import TrainStep
+from gate_reference import GateGradients, gate_inputs
 
 pytestmark = pytest.mark.gpu
 F = torch.float64
@@ -395,6 +396,43 @@ def test_gate_backward(T, hc, d, saved):
 @pytest.mark.parametrize("T,hc,d", [(700, 2, 256), (320, 4, 5120), (3, 8, 9216), (2, 1, 20_736)])
 def test_gate_backward_of_many_and_of_wide_tokens(T, hc, d, saved):
     test_gate_backward(T, hc, d, saved)
+
+
+GRADIENTS = [(7, 1, 256), (9, 2, 512), (5, 4, 1024), (8, 3, 1280), (6, 8, 256), (9, 5, 2816), (12, 4, 5120),
+             (320, 4, 5120), (600, 2, 256), (11, 7, 1280), (7, 1, 20_480), (3, 8, 9216), (7, 1, 20_736)]
+
+
+@pytest.mark.parametrize("saved", ["f32", "bf16", "mxfp8"])
+@pytest.mark.parametrize("T,hc,d", GRADIENTS)
+def test_gate_backward_term_by_term(T, hc, d, saved):
+    """Every gradient to its BF16 rounding and the error of the sums behind it (gate_reference.py):
+    no term of dh or dk could be missing, at any width, from dots of 2e-3 to 30."""
+    h, kv, win, wq, wk, dy, on = gate_inputs(T, hc, d, T)
+    s = make_layer(hc, d, wq=wq, wk=wk)
+    ws = ws_of(eg.engram_gate_backward_workspace_bytes(s.ctx, T))
+    dh = torch.full((T, hc, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dkv = torch.full((T, (hc + 1) * d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dwq, dwk = (torch.full((hc, d), float("nan"), device="cuda") for _ in range(2))
+    to = (win.cuda(), T, dy.cuda(), dh, dkv, dwq, dwk, ws)
+    if saved == "mxfp8":
+        codes, exps = pack_ref(torch.cat([h.float().reshape(T, hc * d), kv], 1))
+        both = unpack_ref(codes, exps)
+        h, kv = both[:, :hc * d].reshape(T, hc, d), both[:, hc * d:]
+        eg.engram_gate_backward_checkpoint(s.ctx, 0, codes.cuda().view(torch.uint8), exps.cuda(), *to)
+    else:
+        kv = kv if saved == "f32" else kv.bfloat16()
+        eg.engram_gate_backward(s.ctx, 0, kv.cuda(), eg.KV_F32 if saved == "f32" else eg.KV_BF16, h.cuda(), *to)
+    eg.engram_sync(s.ctx)
+    ref = GateGradients(h, kv, on, wq, wk, dy)
+    assert ref.misses(dh.cpu(), dkv.cpu()) == []
+    # the weights' sums over the tokens: each term dS h k w as dS, and the additions of up to T
+    # terms, one after the other at the most
+    dS = ref.rho * (ref.first["dh"] * h.to(F)).abs() / wq.to(F).abs()  # (first["dh"] = dS wq wk k)
+    add = T * 2.0 ** -24 * (ref.first["dh"] * h.to(F)).abs() / wq.to(F).abs()
+    tol = (dS + add).sum(0)
+    assert ((dwq.cpu().to(F) - ref.dwq).abs() <= tol).all()
+    assert ((dwk.cpu().to(F) - ref.dwk).abs() <= tol * (wq / wk).abs().to(F)).all()
+    s.close()
 
 
 def test_gate_backward_against_differences():
