@@ -513,7 +513,10 @@ engram_status engram_embed_grad(engram_ctx* ctx, uint64_t rows, uint32_t dim, co
  * [T][hc][d], read; d_hidden_out, written, may be d_hidden; d_gates fp32
  * [T][hc] or NULL; d_codes uint8 [T][(2 hc + 1) d]; d_scales uint8
  * [T][(2 hc + 1) d / 32].  An image row passes through, its kv does not
- * matter and its checkpoint is zero.  All 16-byte aligned, d_gates 4. */
+ * matter and its checkpoint is zero.  All 16-byte aligned, d_gates 4.  A dot
+ * product that is NaN (from an infinity or NaN in hidden or keys) leaves the
+ * max at 1e-6, here as in engram_gate, so the gate is that of a dot of 0; in
+ * the backward pass dv is then finite, dhidden and the keys' part of dkv NaN. */
 engram_status engram_gate_checkpoint(const engram_ctx* ctx, int layer, const void* d_kv,
                                      int kv_format, const uint32_t* d_windows, int64_t T,
                                      const uint16_t* d_hidden, uint16_t* d_hidden_out,

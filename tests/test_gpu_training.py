@@ -299,6 +299,45 @@ def test_gate_checkpoint_of_many_and_of_wide_tokens(T, hc, d, kv_format):
     test_gate_checkpoint(T, hc, d, kv_format)
 
 
+def test_a_dot_that_is_nan_is_taken_for_zero_as_by_engram_gate():
+    """max(|dot|, 1e-6) leaves a NaN out (fmax), in the oracle and in every call of the library: the
+    branch's gate is that of a dot of 0, engram_gate's and the checkpoint's alike; what is infinite
+    or NaN in the activations itself reaches the branch's outputs; other branches and tokens do
+    not see it."""
+    T, hc, d = 3, 2, 512
+    h, kv, win, wq, wk = gate_problem(T, hc, d, 6, image=())
+    kv[1, 5] = float("nan")     # a key of branch 0
+    h[2, 1, 7] = float("inf")   # hidden of branch 1: rh = 0, dot = 0 inf = NaN
+    dy = rnd(9, T, hc, d)
+    s = make_layer(hc, d, wq=wq, wk=wk)
+    plain, pgates = h.cuda(), torch.empty(T, hc, device="cuda")
+    eg.engram_gate(s.ctx, 0, kv.cuda(), win.cuda(), T, plain, pgates)
+    out, gates = torch.empty_like(plain), torch.empty_like(pgates)
+    kept = (2 * hc + 1) * d
+    codes = torch.empty(T, kept, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(T, kept // 32, dtype=torch.uint8, device="cuda")
+    eg.engram_gate_checkpoint(s.ctx, 0, kv.cuda(), eg.KV_F32, win.cuda(), T, h.cuda(), out, gates, codes, scales)
+    ws = ws_of(eg.engram_gate_backward_workspace_bytes(s.ctx, T))
+    dh = torch.empty(T, hc, d, dtype=torch.bfloat16, device="cuda")
+    dkv = torch.empty(T, (hc + 1) * d, dtype=torch.bfloat16, device="cuda")
+    dwq, dwk = (torch.empty(hc, d, device="cuda") for _ in range(2))
+    eg.engram_gate_backward(s.ctx, 0, kv.cuda(), eg.KV_F32, h.cuda(), win.cuda(), T, dy.cuda(), dh, dkv, dwq, dwk,
+                            ws)
+    eg.engram_sync(s.ctx)
+    half = {1 / (1 + math.exp(-1e-3)), 1 / (1 + math.exp(1e-3))}  # a NaN has either sign
+    for t, b in ((1, 0), (2, 1)):
+        for g in (float(gates[t, b]), float(pgates[t, b])):
+            assert min(abs(g - x) for x in half) <= 1e-6
+        dk = dkv[t, b * d:(b + 1) * d].cpu()
+        assert not dk.isfinite().any()
+    ok = torch.ones(T, hc, dtype=torch.bool)
+    ok[1, 0] = ok[2, 1] = False
+    assert (gates.cpu()[ok] - pgates.cpu()[ok]).abs().max() <= 1e-5
+    assert dh.cpu()[ok].isfinite().all() and dkv.cpu()[:, :hc * d].reshape(T, hc, d)[ok].isfinite().all()
+    assert dkv[:, hc * d:].isfinite().all()
+    s.close()
+
+
 def test_gate_calls_refuse_misaligned_pointers():
     s = make_layer()
     A = 1 << 20  # an aligned address that no refused call touches
