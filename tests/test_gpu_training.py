@@ -1014,6 +1014,68 @@ def test_a_step_runs_on_its_stream(given):
     s.close()
 
 
+@pytest.mark.parametrize("T,hc,kv_format", [(130, 2, eg.KV_BF16), (13, 2, eg.KV_F32), (61, 1, eg.KV_BF16)])
+def test_every_gradient_of_a_step(T, hc, kv_format):
+    """Each part of a step against its formula in 64 bits on what the step's part before it left:
+    the scales of the embedding and the rows, the mean's gradient, which buffer goes where."""
+    s, kept, embedding, head = step_model(hc)
+    ids, win, labels, dloss = inputs = step_inputs(s, T, 3)
+    step = TrainStep(s, 0, embedding, head, T + 5, kv_format=kv_format, scale=3.0)
+    loss = run_step(step, inputs)
+    eg.engram_sync(s.ctx)
+    c = lambda x, n=T: x[:n].cpu().to(F)  # noqa: E731
+    K, N, kept_n = s.K, s.N, (2 * hc + 1) * D
+    on = (win.cpu()[:, 0] != -1).to(F).reshape(T, 1, 1)
+    table = kept["table"].view(torch.bfloat16)[:s.rows(0) * 32].view(-1, 32).cpu().to(F)
+    wkv = kept["wkv"].view(torch.bfloat16).view(N, K).cpu().to(F)
+    wq, wk = (kept[n].view(hc, D).cpu().to(F) for n in ("wq", "wk"))
+
+    def near(got, ref, mag, n, roundings=1):
+        assert ((got - ref).abs() <= roundings * 2.0 ** -8 * ref.abs() + n * 2.0 ** -23 * mag).all()
+
+    # forward
+    ref = embedding.cpu().to(F)[ids.cpu().long()] * 3.0
+    near(c(step.hidden), ref.unsqueeze(1).expand(-1, hc, -1), ref.unsqueeze(1).abs(), 1)
+    rows = step.rows[:T].cpu().reshape(-1)
+    emb = table[rows.clamp_min(0).long()] * (rows >= 0).unsqueeze(1)
+    assert torch.equal(c(step.emb), emb.reshape(T, K))
+    text = on.reshape(T) == 1
+    ref = c(step.emb) @ wkv.T
+    near(c(step.kv)[text], ref[text], (c(step.emb).abs() @ wkv.T.abs())[text], K)
+    saved = unpack_ref(step.codes[:T].cpu().view(torch.float8_e4m3fn), step.scales[:T].cpu())
+    near(c(step.x), c(step.out).mean(1), c(step.out).abs().mean(1), hc)
+    z = c(step.x) @ head.cpu().to(F).T
+    lse, y = torch.logsumexp(z, 1), labels.cpu().long()
+    again = torch.empty_like(loss)  # (the loss itself has tests of its own)
+    eg.engram_loss(s.ctx, step.x, head, VOCAB, D, labels, T, again, None,
+                   ws_of(eg.engram_loss_workspace_bytes(T, VOCAB, D)))
+    eg.engram_sync(s.ctx)
+    assert torch.equal(loss, again)
+    # backward
+    dz = torch.exp(z - lse.unsqueeze(1))
+    dz[torch.arange(T), y.clamp_min(0)] -= 1
+    dz *= (dloss.cpu().to(F) * (y >= 0)).unsqueeze(1)
+    for got, a, b, n in ((c(step.dx), dz, head.cpu().to(F), VOCAB), (step.dhead.cpu().to(F), dz.T, c(step.x), T)):
+        mag = a.abs() @ b.abs()
+        assert ((got - a @ b).abs() <= 2.0 ** -8 * ((a @ b).abs() + mag) + n * 2.0 ** -23 * mag).all()
+    dout = (step.dx[:T].float() / hc).bfloat16().cpu().unsqueeze(1).expand(-1, hc, -1)
+    gate = GateGradients(saved[:, :hc * D].reshape(T, hc, D), saved[:, hc * D:], on, wq, wk, dout)
+    assert gate.misses(step.dhidden[:T].cpu(), step.dkv[:T].cpu()) == []
+    for got, ref in ((step.dwq, gate.dwq), (step.dwk, gate.dwk)):
+        tol = ((gate.rho + T * 2.0 ** -24) * (gate.first["dh"] * saved[:, :hc * D].reshape(T, hc, D)).abs()).sum(0)
+        assert ((got.cpu().to(F) - ref).abs() <= 4 * tol).all()  # (wq and wk are between 0.5 and 2)
+    dkv = c(step.dkv)
+    near(c(step.demb), dkv @ wkv, dkv.abs() @ wkv.abs(), N)
+    near(step.dwkv.cpu().to(F), dkv.T @ c(step.emb), dkv.T.abs() @ c(step.emb).abs(), T)
+    for ids_, dout, n, scale, unique, count, grad in (
+            (ids.cpu(), step.dhidden[:T].cpu(), VOCAB, 3.0, step.token_ids, step.token_count, step.token_grad),
+            (rows, step.demb[:T].cpu().reshape(-1, 1, 32), s.rows(0), 1.0, step.row_ids, step.row_count, step.row_grad)):
+        u, ref, tol = grad_reference(ids_.long(), dout, n, scale)
+        assert int(count) == u.numel() and torch.equal(unique[:u.numel()].cpu().long(), u)
+        assert ((grad[:u.numel()].cpu().to(F) - ref).abs() <= tol).all()
+    s.close()
+
+
 def test_training_example_learns():
     import importlib.util
     import os
