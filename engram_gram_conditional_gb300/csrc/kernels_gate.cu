@@ -7,9 +7,11 @@
 // So a cluster of CTAs keeps a token in shared memory between the two.  At hc 4,
 // d 5,120 and 2,048 tokens (GB300, copy bandwidth 6.77 TB/s): forward with fp32
 // kv 86 us (475 MB, 81%; a block per token that reads hidden again 97), with BF16
-// kv 76; backward from the checkpoint 81 us (370 MB, 67%: the kernel 75, bound by
-// HBM and by its issue rate, and the weights' sums 6; two kernels over the tokens
-// 214), from BF16 kv 89, from fp32 kv 111.
+// kv 76; backward from the checkpoint 81 us (370 MB, 67%: the kernel 75, neither HBM
+// nor its issue slots full, and the weights' sums 6; two kernels over the tokens
+// 214), from BF16 kv 89, from fp32 kv 111.  With 5 to 8 branches the backward kernel
+// spills 150 to 320 bytes a thread: from the checkpoint 115 us at hc 8, d 2,560 and
+// 172 at hc 5, d 4,096, where the bytes take 52 and 54.
 #include <algorithm>
 
 #include "grad_internal.h"

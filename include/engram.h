@@ -563,7 +563,7 @@ engram_status engram_project_backward(const engram_ctx* ctx, int layer, const ui
  * (fp32 [T], each may be NULL).  d_x bf16 [T][dim]; d_head bf16 [vocab][dim];
  * d_labels int32 [T]: a negative label is ignored (loss 0), one >= vocab is
  * too and sets the error word (ENGRAM_EBOUNDS).  dim: a multiple of 8 up to
- * 65,536; any vocab.  d_x, d_head 16-byte aligned.
+ * 65,536; vocab up to 2^30.  d_x, d_head 16-byte aligned.
  * d_workspace: engram_loss_workspace_bytes(T, vocab, dim) bytes. */
 size_t engram_loss_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim);
 engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* d_head,
@@ -574,7 +574,8 @@ engram_status engram_loss(engram_ctx* ctx, const uint16_t* d_x, const uint16_t* 
  * ignored) is kept as BF16, in units of dloss[0], for that piece only, and dx =
  * dz head (bf16 [T][dim]) and dhead = dz^T x (bf16 [vocab][dim], written) are
  * summed in fp32 and rounded once.  d_lse: engram_loss's; d_dloss fp32 [T]; d_dx or d_dhead
- * may be NULL.  d_workspace: engram_loss_backward_workspace_bytes(T, vocab, dim)
+ * may be NULL.  A label >= vocab is ignored as a negative one is; engram_loss
+ * reports it.  d_workspace: engram_loss_backward_workspace_bytes(T, vocab, dim)
  * bytes: the piece's dz (about 64 MB, 8 KB per token for a very long batch)
  * and the fp32 dx (one, or parts of it within 64 MB). */
 size_t engram_loss_backward_workspace_bytes(int64_t T, uint32_t vocab, uint32_t dim);
