@@ -28,7 +28,8 @@ OK, EINVAL, ENOMEM, ECUDA, ESTATE, ETIMEOUT, EUNSUPPORTED, EBOUNDS = range(8)
 # Names exported by the library (the declarations of include/engram.h).
 EXPORTS = (
     "engram_ctx_create", "engram_ctx_destroy", "engram_layer_params",
-    "engram_layer_set_multipliers", "engram_layer_bind", "engram_layer_info",
+    "engram_layer_set_multipliers", "engram_layer_bind", "engram_layer_refresh",
+    "engram_layer_info",
     "engram_table_fill", "engram_table_fill_bf16",
     "engram_session_create", "engram_session_fork", "engram_session_reset",
     "engram_session_destroy", "engram_session_append", "engram_batch_append",
@@ -133,6 +134,7 @@ def lib() -> C.CDLL:
             "engram_layer_params": [vp, C.c_int, vp, vp, vp, vp],
             "engram_layer_set_multipliers": [vp, C.c_int, vp],
             "engram_layer_bind": [vp, C.c_int, C.POINTER(LayerWeights)],
+            "engram_layer_refresh": [vp, C.c_int, vp],
             "engram_layer_info": [vp, C.c_int, C.POINTER(LayerInfo)],
             "engram_table_fill": [vp, C.c_uint64, vp, vp, C.c_uint64, C.c_uint64, vp],
             "engram_table_fill_bf16": [vp, C.c_uint64, vp, C.c_uint64, C.c_uint64, vp],
@@ -280,6 +282,10 @@ def engram_layer_set_multipliers(ctx, layer: int, mult):
 def engram_layer_bind(ctx, layer: int, table, scales, rows: int, wkv, wq, wk, flags: int = 0):
     w = LayerWeights(_ptr(table), _ptr(scales), rows, _ptr(wkv), _ptr(wq), _ptr(wk), flags)
     _check(lib().engram_layer_bind(ctx, layer, C.byref(w)))
+
+
+def engram_layer_refresh(ctx, layer: int, stream=None):
+    _check(lib().engram_layer_refresh(ctx, layer, _stream(stream)))
 
 
 def engram_layer_info(ctx, layer: int) -> dict:

@@ -688,6 +688,20 @@ engram_status bind_impl(engram_ctx* ctx, int layer, const engram_layer_weights* 
 }
 }  // namespace
 
+engram_status engram_layer_refresh(const engram_ctx* ctx, int layer, void* stream) {
+    engram_status st = check_layer(ctx, layer, true);
+    if (st) return st;
+    const LayerState& L = ctx->layers[layer];
+    if (L.f16)
+        return fail(ENGRAM_EUNSUPPORTED, "a layer on FP16 operands has to be bound again (engram_layer_bind)");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (ctx->device != dev) return fail(ENGRAM_ESTATE, "context bound on another device");
+    e = launch_mul_f32(L.w.wq, L.w.wk, L.wqk, (int64_t)ctx->desc.hc * ctx->desc.d, (cudaStream_t)stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "w_q w_k product");
+}
+
 engram_status engram_layer_info(const engram_ctx* ctx, int layer, engram_layer_info_t* out) {
     engram_status st = check_layer(ctx, layer, false);
     if (st) return st;

@@ -13,8 +13,8 @@ import numpy as np
 import torch
 
 from . import (BIND_TABLE_BF16, engram_ctx_create, engram_ctx_destroy, engram_host_table_alloc,
-               engram_host_table_free, engram_layer_bind, engram_layer_params, engram_table_fill,
-               engram_table_fill_bf16)
+               engram_host_table_free, engram_layer_bind, engram_layer_info, engram_layer_params,
+               engram_layer_refresh, engram_table_fill, engram_table_fill_bf16)
 
 
 def _round16(n: int) -> int:
@@ -45,6 +45,7 @@ class EngramLayerSet:
         self.params = [engram_layer_params(self.ctx, l, self.nb) for l in range(self.n_layers)]
         self.tensors = [dict() for _ in range(self.n_layers)]
         self._flags = [0] * self.n_layers
+        self.outdated = set()  # layers whose weights changed since they were bound
         self._host = []  # (address, bytes) of host tables from engram_host_table_alloc
 
     @classmethod
@@ -103,6 +104,7 @@ class EngramLayerSet:
         self.tensors[layer] = dict(table=table, scales=scales, wkv=d_wkv, wq=d_wq, wk=d_wk,
                                    table_seed=table_seed)
         self._flags[layer] = flags
+        self.outdated.discard(layer)
         return self.tensors[layer]
 
     def rebind(self, layer: int):
@@ -112,6 +114,18 @@ class EngramLayerSet:
         t = self.tensors[layer]
         engram_layer_bind(self.ctx, layer, t["table"], t["scales"], self.rows(layer), t["wkv"], t["wq"],
                           t["wk"], self._flags[layer])
+        self.outdated.discard(layer)
+
+    def fp16_operands(self, layer: int) -> bool:
+        """Whether the layer works on FP16 operands: what it keeps of its weights, an FP16 copy of wkv and
+        the exponents of an MXFP8 table, is made by a bind alone (BIND_BF16_OPERANDS: it does not)."""
+        return bool(engram_layer_info(self.ctx, layer)["fp16_operands"])
+
+    def refresh(self, layer: int, stream=None):
+        """After a change of the layer's tensors: make what a layer on BF16 operands keeps of them (the
+        product of the norm weights) again on `stream`.  It may be captured, and what was captured
+        before it uses the new values too."""
+        engram_layer_refresh(self.ctx, layer, stream)
 
     def close(self):
         if self.ctx is not None:

@@ -134,6 +134,8 @@ class TrainStep:
         if not 0 < T <= self.tokens:
             raise ValueError(f"{T} tokens: 1 to {self.tokens} are possible")
         self._check_step(ids, windows, labels, T)
+        if layer in self.model.outdated:
+            raise ValueError("the layer's weights changed since it was bound: model.rebind(layer) first")
         self.T, stream = T, self._on(stream)
         engram_embed(ctx, self.embedding, EMBED_BF16, self.vocab, self.d, ids, T, self.scale, self.hc,
                      self.hidden, stream)
@@ -274,13 +276,22 @@ class AdamW:
             self.lr.fill_(float(lr))
 
     def step(self, stream=None, rebind=True):
-        """One update with the gradients of the last backward().  ``rebind``: wait for it and bind the
-        layer again, as its next use needs; a captured step is made without, and the layer bound
-        (``model.rebind(layer)``) after its replays."""
+        """One update with the gradients of the last backward().
+
+        The layer's next use needs what it keeps of its weights made again.  ``rebind``: wait for the
+        update and bind the layer.  Without, nothing waits, as a captured step needs: a layer on BF16
+        operands (a BF16 table, or bound with BIND_BF16_OPERANDS) is refreshed on the stream, and a
+        captured step's replays follow one another like eager ones.  One on FP16 operands has to be
+        bound (``model.rebind(layer)``) before its next forward(), which refuses until then; such a
+        step is not captured."""
         t = self.train
         if t.T == 0:
             raise ValueError("no backward() whose gradients could be used")
         ctx, stream = t.model.ctx, t._on(stream)
+        fp16 = t.model.fp16_operands(t.layer)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing() and (rebind or fp16):
+                raise ValueError("a captured step: rebind=False, and a layer on BF16 operands (BIND_BF16_OPERANDS)")
         engram_grad_norm(ctx, self._parts, self.max_norm, self.norms, self.norm, self.factor, self.ws, stream)
         with torch.cuda.stream(stream):
             self.steps += torch.isfinite(self.norm)
@@ -294,3 +305,7 @@ class AdamW:
         if rebind:
             stream.synchronize()
             t.model.rebind(t.layer)
+        elif fp16:
+            t.model.outdated.add(t.layer)
+        else:
+            t.model.refresh(t.layer, stream)

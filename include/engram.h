@@ -179,6 +179,14 @@ engram_status engram_layer_set_multipliers(engram_ctx* ctx, int layer, const uin
  * gate uses the two only through it: bind again after changing them) and
  * encodes the TMA descriptors.  It synchronises the device. */
 engram_status engram_layer_bind(engram_ctx* ctx, int layer, const engram_layer_weights* w);
+/* Make the product w_q w_k again from the arrays that the layer is bound to, on `stream` and in its
+ * place: what comes after it on the stream, launches captured before it among them, uses the new
+ * w_q and w_k.  It allocates nothing, does not synchronise and may be captured: the last part of a
+ * training step whose graph is replayed.  Everything else that a layer on BF16 operands uses it
+ * reads from the bound arrays.  A layer on FP16 operands (engram_layer_info's fp16_operands) also
+ * holds a copy of wkv and the exponents of its table: ENGRAM_EUNSUPPORTED; it is bound again, or
+ * was to be bound with ENGRAM_BIND_BF16_OPERANDS. */
+engram_status engram_layer_refresh(const engram_ctx* ctx, int layer, void* stream);
 
 /* Fill rows [row_begin, row_end) of a table with its deterministic contents:
  * code(row, col) and scale(row, group) are a Philox4x32-10 function of

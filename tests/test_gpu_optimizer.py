@@ -1,0 +1,120 @@
+"""Training steps with an optimizer that follow one another: what a layer keeps of its weights, eager and
+captured."""
+import math
+
+import pytest
+import torch
+
+import engram_gram_conditional_gb300 as eg
+from engram_gram_conditional_gb300.training import AdamW, TrainStep
+from test_gpu_update import step_inputs, step_model
+
+pytestmark = pytest.mark.gpu
+
+
+def made(mx_table, flags=0, T=40, **kw):
+    s, kept, embedding, head, norm = step_model(mx_table)
+    if flags:
+        s._flags[0] |= flags
+        s.rebind(0)
+    step = TrainStep(s, 0, embedding, head, T, norm=norm)
+    opt = AdamW(step, 1e-2, max_norm=5.0, weight_decay=0.1, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    return s, kept, step, opt, side, step_inputs(s, T, 2)
+
+
+def exponent(x):
+    return math.frexp(float(x.view(torch.bfloat16).abs().max()))[1]
+
+
+@pytest.mark.parametrize("mx_table", [False, True])
+def test_replays_of_a_captured_step_are_eager_steps(mx_table):
+    """Forward, backward and update, replayed, against eager steps that bind the layer each time: every
+    step sees all weights as the one before left them (with an MXFP8 table the largest |wkv| passes a
+    power of two)."""
+    results = []
+    for captured in (False, True):
+        s, kept, step, opt, side, inputs = made(mx_table, eg.BIND_BF16_OPERANDS if mx_table else 0,
+                                                lr_scale=dict(table=300.0))
+        begin = exponent(kept["wkv"]), kept["wq"].clone(), kept["table"].clone()
+        seen = []
+
+        def once(rebind):
+            step.forward(*inputs[:3], side)
+            step.backward(*inputs, side)
+            opt.step(side, rebind=rebind)
+
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                once(False)
+        for _ in range(4):
+            graph.replay() if captured else once(True)
+            torch.cuda.synchronize()
+            seen += [x.clone() for x in (step.loss, step.kv, step.gates, step.dwq, step.dwkv, step.dhidden)]
+        eg.engram_sync(s.ctx)
+        assert int(opt.steps) == 4
+        assert not torch.equal(begin[1], kept["wq"]) and not torch.equal(begin[2], kept["table"])
+        assert not mx_table or exponent(kept["wkv"]) > begin[0]  # (its weights are small: the rate takes them there)
+        results.append(seen + [x.clone() for x in (step.head, step.embedding, step.norm, kept["wkv"], kept["wq"],
+                                                   kept["wk"], kept["table"])])
+        s.close()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    losses = results[1][::6][:4]
+    assert not torch.equal(losses[0], losses[1]) and not torch.equal(losses[1], losses[2])
+
+
+def test_steps_without_a_bind_are_steps_with_one():
+    """A layer on BF16 operands is refreshed on the stream; nothing else of it is kept."""
+    results = []
+    for rebind in (True, False):
+        s, kept, step, opt, side, inputs = made(True, eg.BIND_BF16_OPERANDS)
+        for _ in range(3):
+            step.forward(*inputs[:3], side)
+            step.backward(*inputs, side)
+            opt.step(side, rebind=rebind)
+        torch.cuda.synchronize()
+        eg.engram_sync(s.ctx)
+        results.append([x.clone() for x in (step.loss, step.gates, kept["wkv"], kept["wq"], kept["table"])])
+        s.close()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_a_layer_on_fp16_operands_is_bound_between_steps():
+    """What such a layer keeps is made by a bind alone: a step without one holds up the next
+    forward(), and is not captured."""
+    s, kept, step, opt, side, inputs = made(True)
+    assert s.fp16_operands(0)
+    with pytest.raises(eg.EngramError) as e:
+        s.refresh(0)
+    assert e.value.status == eg.EUNSUPPORTED
+    step.forward(*inputs[:3], side)
+    step.backward(*inputs, side)
+    torch.cuda.synchronize()
+    before = kept["wq"].clone()
+    for rebind in (False, True):
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(ValueError, match="captured"):
+            with torch.cuda.graph(graph, stream=side):
+                opt.step(side, rebind=rebind)
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 0 and torch.equal(before, kept["wq"])
+    opt.step(side, rebind=False)
+    with pytest.raises(ValueError, match="rebind"):
+        step.forward(*inputs[:3], side)
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 1 and not torch.equal(before, kept["wq"])
+    s.rebind(0)
+    step.forward(*inputs[:3], side)
+    got = step.loss.clone()
+    # the same step with the bind in it
+    t, _, step2, opt2, _, _ = made(True)
+    step2.forward(*inputs[:3], side)
+    step2.backward(*inputs, side)
+    opt2.step(side)
+    step2.forward(*inputs[:3], side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, step2.loss)
+    s.close()
+    t.close()

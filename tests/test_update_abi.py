@@ -254,3 +254,24 @@ def test_lists_and_structs_keep_their_tensors():
     kept.clear()
     gc.collect()
     assert all(x() is None for x in seen)
+
+
+def test_refresh_refuses(ctx):
+    refused(eg.EINVAL, eg.engram_layer_refresh, None, 0)
+    refused(eg.EINVAL, eg.engram_layer_refresh, ctx, 1)
+    refused(eg.EINVAL, eg.engram_layer_refresh, ctx, -1)
+    refused(eg.ESTATE, eg.engram_layer_refresh, ctx, 0)  # not bound
+
+
+def test_a_step_on_an_outdated_layer_is_refused():
+    from types import SimpleNamespace
+
+    from engram_gram_conditional_gb300.training import TrainStep
+
+    step = object.__new__(TrainStep)  # (its buffers need a GPU; what is refused reaches none)
+    step.model = SimpleNamespace(device=torch.device("cpu"), ctx=None, outdated={1})
+    step.layer, step.tokens, step.T = 1, 8, 0
+    i32 = torch.int32
+    with pytest.raises(ValueError, match="rebind"):
+        step.forward(torch.zeros(5, dtype=i32), torch.zeros(5, 4, dtype=i32), torch.zeros(5, dtype=i32))
+    assert step.T == 0
