@@ -626,10 +626,6 @@ engram_status bind_impl(engram_ctx* ctx, int layer, const engram_layer_weights* 
     e = launch_mul_f32(w->wq, w->wk, L.wqk, nqk, 0);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "w_q w_k product");
-    if (L.wkv_f16) {
-        cudaFree(L.wkv_f16);
-        L.wkv_f16 = nullptr;
-    }
     L.f16 = false;
     if (want_f16 && scales_fit && w_finite) {
         // exponent shift: all decoded values FP16-normal when the span allows
@@ -643,11 +639,14 @@ engram_status bind_impl(engram_ctx* ctx, int layer, const engram_layer_weights* 
             frexpf(maxabs, &ex);  // maxabs < 2^ex
             wexp = 15 - ex;
         }
-        const size_t bytes = (size_t)ctx->N * ctx->K * sizeof(uint16_t);
-        e = cudaMalloc(&L.wkv_f16, bytes);
-        if (e != cudaSuccess) {
-            L.wkv_f16 = nullptr;
-            return fail(ENGRAM_ENOMEM, "cudaMalloc of the FP16 wkv copy");
+        // the copy stays where it is over later binds, whatever path they take: launches that were
+        // captured into a graph read it there
+        if (!L.wkv_f16) {
+            e = cudaMalloc(&L.wkv_f16, (size_t)ctx->N * ctx->K * sizeof(uint16_t));
+            if (e != cudaSuccess) {
+                L.wkv_f16 = nullptr;
+                return fail(ENGRAM_ENOMEM, "cudaMalloc of the FP16 wkv copy");
+            }
         }
         // the copy is stored as 128 x 64 tiles, each 16 KB contiguous: one
         // tensor map over them, viewed as [N K / 64][64] with 128-row boxes,
@@ -661,11 +660,7 @@ engram_status bind_impl(engram_ctx* ctx, int layer, const engram_layer_weights* 
         if (e == cudaSuccess)
             e = make_tma_16bit(&L.tm_wkv_f16_2k, L.wkv_f16, (uint64_t)ctx->N * ctx->K / kBK, kBK,
                                kBN, true);
-        if (e != cudaSuccess) {
-            cudaFree(L.wkv_f16);
-            L.wkv_f16 = nullptr;
-            return cuda_fail(e, "FP16 wkv copy");
-        }
+        if (e != cudaSuccess) return cuda_fail(e, "FP16 wkv copy");
         L.f16 = true;
         L.wkv_exp = wexp;
         L.a_exp_shift = shift;

@@ -107,14 +107,21 @@ class EngramLayerSet:
         self.outdated.discard(layer)
         return self.tensors[layer]
 
-    def rebind(self, layer: int):
+    def rebind(self, layer: int) -> bool:
         """Bind the layer's tensors again after their contents changed: the product of the norm
         weights and the bind-time scans follow them.  The changes are done on the device when this
-        is called; it synchronises the device."""
-        t = self.tensors[layer]
+        is called; it synchronises the device.  True: what was captured of the layer since the bind
+        before has to be captured again (its operands' type or exponents are others); otherwise it
+        holds, and its replays use the new contents."""
+        def held():
+            return [engram_layer_info(self.ctx, layer)[k] for k in ("fp16_operands", "wkv_exp", "a_exp_shift")]
+
+        t, before = self.tensors[layer], held()
         engram_layer_bind(self.ctx, layer, t["table"], t["scales"], self.rows(layer), t["wkv"], t["wq"],
                           t["wk"], self._flags[layer])
         self.outdated.discard(layer)
+        after = held()
+        return after[0] != before[0] or bool(after[0]) and after != before
 
     def fp16_operands(self, layer: int) -> bool:
         """Whether the layer works on FP16 operands: what it keeps of its weights, an FP16 copy of wkv and

@@ -279,7 +279,8 @@ class AdamW:
         """One update with the gradients of the last backward().
 
         The layer's next use needs what it keeps of its weights made again.  ``rebind``: wait for the
-        update and bind the layer.  Without, nothing waits, as a captured step needs: a layer on BF16
+        update and bind the layer (and return what ``model.rebind`` does: True where what was captured
+        of the layer has to be captured again).  Without, nothing waits, as a captured step needs: a layer on BF16
         operands (a BF16 table, or bound with BIND_BF16_OPERANDS) is refreshed on the stream, and a
         captured step's replays follow one another like eager ones.  One on FP16 operands has to be
         bound (``model.rebind(layer)``) before its next forward(), which refuses until then; such a
@@ -304,8 +305,9 @@ class AdamW:
                           step, stream)
         if rebind:
             stream.synchronize()
-            t.model.rebind(t.layer)
-        elif fp16:
+            return t.model.rebind(t.layer)
+        if fp16:
             t.model.outdated.add(t.layer)
         else:
             t.model.refresh(t.layer, stream)
+        return False

@@ -34,8 +34,8 @@
  *    word and bind-time scan results, allocated at the first
  *    engram_layer_bind), per bound layer the elementwise product of w_q and
  *    w_k (hc x d x 4 bytes) and, on the FP16 operand path, an FP16 copy of
- *    wkv (N x K x 2 bytes), allocated by engram_layer_bind and freed by a
- *    rebind (the FP16 copy) or engram_ctx_destroy.
+ *    wkv (N x K x 2 bytes), allocated by the first engram_layer_bind that
+ *    needs them, kept by later ones and freed by engram_ctx_destroy.
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *    Device calls are asynchronous on that stream.  Faults found by a kernel
  *    (a row index outside the table, a wait that ran out) set the context's
@@ -177,7 +177,11 @@ engram_status engram_layer_set_multipliers(engram_ctx* ctx, int layer, const uin
  * exponents and wkv's magnitude, builds the FP16 copy of wkv when the FP16
  * operand path applies (engram_layer_info), keeps the product w_q w_k (the
  * gate uses the two only through it: bind again after changing them) and
- * encodes the TMA descriptors.  It synchronises the device. */
+ * encodes the TMA descriptors.  It synchronises the device.
+ * Launches of the layer that were captured into a graph hold what the bind gave them: the arrays'
+ * and the copies' addresses, which a bind to the same arrays leaves as they are, and on the FP16
+ * operand path the exponents.  Where a bind changes fp16_operands, wkv_exp or a_exp_shift
+ * (engram_layer_info), or the arrays, they are captured again before their next replay. */
 engram_status engram_layer_bind(engram_ctx* ctx, int layer, const engram_layer_weights* w);
 /* Make the product w_q w_k again from the arrays that the layer is bound to, on `stream` and in its
  * place: what comes after it on the stream, launches captured before it among them, uses the new

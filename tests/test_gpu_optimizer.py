@@ -118,3 +118,52 @@ def test_a_layer_on_fp16_operands_is_bound_between_steps():
     assert torch.equal(got, step2.loss)
     s.close()
     t.close()
+
+
+def test_a_captured_forward_holds_over_binds():
+    """On FP16 operands: the copy of wkv stays where a graph reads it, also while the layer is bound to
+    a table that takes BF16 operands; where exponents change, the bind says so."""
+    s, kept, step, opt, side, inputs = made(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step.forward(*inputs[:3], side)
+
+    def replay():
+        graph.replay()
+        torch.cuda.synchronize()
+        return step.kv.clone(), step.loss.clone()
+
+    def eager():
+        step.forward(*inputs[:3], side)
+        torch.cuda.synchronize()
+        return step.kv.clone(), step.loss.clone()
+
+    def same(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+
+    first = replay()
+    assert same(first, eager())
+    # other values of the same size: replays see them
+    kept["wkv"].view(torch.bfloat16).neg_()
+    kept["wq"].mul_(1.5)
+    assert not s.rebind(0)
+    changed = replay()
+    assert same(changed, eager()) and not torch.equal(first[0], changed[0])
+    # a scale far from the others takes the layer off FP16 operands, and back
+    scale = int(kept["scales"][0])
+    kept["scales"][0] = 30
+    assert s.rebind(0) and not s.fp16_operands(0)
+    hold = [torch.full((kept["wkv"].numel(),), -1, dtype=torch.int16, device="cuda") for _ in range(8)]
+    kept["scales"][0] = scale
+    assert s.rebind(0) and s.fp16_operands(0)
+    assert same(replay(), changed) and len(hold) == 8
+    # another exponent of wkv: captured again
+    kept["wkv"].view(torch.bfloat16).mul_(4)
+    assert s.rebind(0)
+    graph.reset()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step.forward(*inputs[:3], side)
+    assert same(replay(), eager())
+    eg.engram_sync(s.ctx)
+    s.close()
