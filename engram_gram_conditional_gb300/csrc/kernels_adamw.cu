@@ -171,17 +171,16 @@ __device__ __forceinline__ void noise8(const AdamwStep& h, uint64_t place8, uint
 
 // A step of 16 values; the states' codes and exponents in place.  take(half, p, g) gives the
 // parameters and gradients of 8 of them, give(half, p) gets the new parameters: no more
-// than 8 are held at a time.  Scaling by a power of two is exact, so that codes are scaled,
-// decayed (and squared) in one product.
+// than 8 are held at a time.  Gradients and roots take their factor and scale before they are
+// squared: the squares of a small factor or scale alone leave fp32's range long before v does.
 template <class Take, class Give>
 __device__ __forceinline__ void step16(const AdamwStep& h, const Rates& q, float kept, float rate, uint64_t place,
                                        uint32_t tensor, uint4& mc, uint4& vc, uint32_t& me, uint32_t& ve, Take take,
                                        Give give) {
     f32x2 m[8], r[8];
     {
-        const float sm = e8m0_to_f32(me), sv = e8m0_to_f32(ve);
-        const f32x2 mb = twice(sm * h.b1), vb = twice(sv * sv * h.b2);
-        const f32x2 nb1 = twice(h.nb1 * q.factor), nb2 = twice(h.nb2 * q.factor * q.factor);
+        const f32x2 sm = twice(e8m0_to_f32(me) * h.b1), sv = twice(e8m0_to_f32(ve));
+        const f32x2 factor = twice(q.factor), nb1 = twice(h.nb1), b2 = twice(h.b2), nb2 = twice(h.nb2);
         const f32x2 rc2 = twice(q.rc2), eps = twice(h.eps);
         const f32x2 keep = twice(kept), lr = twice(-rate);
 #pragma unroll
@@ -193,9 +192,11 @@ __device__ __forceinline__ void step16(const AdamwStep& h, const Rates& q, float
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = 4 * half + i;
-                m[j] = fma2(g[i], nb1, mul2(m[j], mb));
-                const float2 v = unpair(fma2(mul2(g[i], g[i]), nb2, mul2(mul2(r[j], r[j]), vb)));
-                r[j] = pair(root(v.x), root(v.y));
+                const f32x2 f = mul2(g[i], factor);
+                r[j] = mul2(r[j], sv);
+                m[j] = fma2(f, nb1, mul2(m[j], sm));
+                const f32x2 v = fma2(mul2(f, f), nb2, mul2(mul2(r[j], r[j]), b2));
+                r[j] = pair(root(unpair(v).x), root(unpair(v).y));
                 const float2 den = unpair(fma2(r[j], rc2, eps));
                 p[i] = fma2(p[i], keep, mul2(mul2(m[j], pair(inverse(den.x), inverse(den.y))), lr));
             }
