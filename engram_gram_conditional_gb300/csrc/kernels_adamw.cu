@@ -68,17 +68,29 @@ __device__ __forceinline__ void step1(const AdamwStep& h, const Rates& q, float 
 // SM's issue slots for it, of which a thread's 8 values one by one took 87; two values an
 // instruction, and 16 to share what a block costs, take 37.
 
-// The root of a value that is not negative, off by up to 2^-23 of itself (a step of Newton's
-// takes wkv and head from 1.22 to 1.28 ms; a code keeps 3 bits).
-__device__ __forceinline__ float root(float v) {
+// 1 / sqrt(v) and 1 / v, off by up to 2^-22 and 2^-23 of themselves.
+__device__ __forceinline__ float inverse_root(float v) {
     float r;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 __device__ __forceinline__ float inverse(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+// Roots of values that are not negative (of those below 2^-126 less than the root), by a step of
+// Newton's from s = v y, y about 1 / sqrt(v): s + (v - s^2) y / 2, whose remainder an fma gives
+// exactly (Markstein, IBM J. Res. Dev. 34, 1990).  What is then rounded is off by 2^-43 of the root:
+// it is the nearest fp32 number but for one value in some 10^5.  Codes and scales are made of it: of
+// 1.02 billion values one code differs from those of rounded roots; with an approximate root 122 and
+// two blocks' scales did.  820M BF16 values take 1,283 us (the approximate root 1,237, sqrtf 1,403),
+// 61M 106 (102, 117); rows and tensors with masters what they took.
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+    const float2 a = unpair(v);
+    const f32x2 y = pair(inverse_root(fmaxf(a.x, 0x1p-126f)), inverse_root(fmaxf(a.y, 0x1p-126f)));
+    const float2 s = unpair(mul2(v, y));
+    return fma2(pair(fmaf(-s.x, s.x, a.x), fmaf(-s.y, s.y, a.y)), mul2(y, twice(0.5f)), pair(s.x, s.y));
 }
 __device__ __forceinline__ float low3(float a, float b, float c) {
     float r;
@@ -195,8 +207,9 @@ __device__ __forceinline__ void step16(const AdamwStep& h, const Rates& q, float
                 const f32x2 f = mul2(g[i], factor);
                 r[j] = mul2(r[j], sv);
                 m[j] = fma2(f, nb1, mul2(m[j], sm));
-                const f32x2 v = fma2(mul2(f, f), nb2, mul2(mul2(r[j], r[j]), b2));
-                r[j] = pair(root(unpair(v).x), root(unpair(v).y));
+                r[j] = root2(fma2(mul2(f, f), nb2, mul2(mul2(r[j], r[j]), b2)));
+                // (a quotient off by 2^-22 of a step that is a small part of p: one more mended by
+                // Newton's step changes 25 of 820M BF16 parameters and takes 4 %)
                 const float2 den = unpair(fma2(r[j], rc2, eps));
                 p[i] = fma2(p[i], keep, mul2(mul2(m[j], pair(inverse(den.x), inverse(den.y))), lr));
             }

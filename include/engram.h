@@ -671,7 +671,7 @@ engram_status engram_grad_norm(const engram_ctx* ctx, const engram_grad_part* pa
  * bits a value, those of Philox4x32-10 with key seed and counter (place / 8, number of the
  * tensor in the list, step), place the value's index in its tensor or table; the same
  * arguments give the same codes.  A positive root never takes code 0 (a v below fp32's normal
- * range counts as 0).  Values stay in fp32's range: |factor grad| and |grad| below 1e19. */
+ * range counts as less than it is, down to 0).  Values stay in fp32's range: |factor grad| and |grad| below 1e19. */
 typedef struct engram_adamw_step {
     double lr, beta1, beta2, eps; /* betas in [0, 1), eps a positive normal fp32 number */
     uint64_t seed;
