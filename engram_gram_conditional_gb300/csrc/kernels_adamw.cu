@@ -53,13 +53,13 @@ __device__ __forceinline__ Rates rates_of(const AdamwStep& h) {
     return r;
 }
 
-// A step on fp32 states, in place.  (The quotient is off by two units in the last place.)
+// A step on fp32 states, in place; the root and the quotient are rounded.
 __device__ __forceinline__ void step1(const AdamwStep& h, const Rates& q, float keep, float lr, float& p, float g,
                                       float& m, float& v) {
     const float f = g * q.factor;
     m = fmaf(f, h.nb1, m * h.b1);
     v = fmaf(f * f, h.nb2, v * h.b2);
-    p = p * keep - lr * __fdividef(m, fmaf(sqrtf(v), q.rc2, h.eps));
+    p = p * keep - lr * (m / fmaf(sqrtf(v), q.rc2, h.eps));
 }
 
 // ---- 8-bit states ---------------------------------------------------------------------------

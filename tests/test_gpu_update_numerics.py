@@ -90,3 +90,21 @@ def test_8_bit_states_are_those_of_rounded_values(ctx):  # noqa: F811
     want = codes_of((torch.from_numpy(m), torch.from_numpy(np.sqrt(v))), np.arange(n), step, seed)
     for name, (codes, scales) in zip("mv", want):
         assert torch.equal(t[name].cpu(), codes) and torch.equal(t[name + "_scales"].cpu(), scales), name
+
+
+def test_fp32_steps_round_their_quotient(ctx):  # noqa: F811
+    """With betas and a parameter of 0 and a rate of 1 the new parameter is -g / (|g| + eps): one sum and
+    one quotient, each rounded to fp32."""
+    n, hyper = 1 << 16, dict(lr=1.0, beta1=0.0, beta2=0.0, eps=0.3)
+    g = rnd(5, n)
+    want = torch.from_numpy(-(g.numpy() / (np.abs(g.numpy()) + np.float32(0.3))))
+    zeros = lambda: torch.zeros(n, device="cuda")  # noqa: E731
+    t = dict(param=zeros(), grad=g.cuda(), m=zeros(), v=zeros())
+    eg.engram_adamw(ctx, eg.adamw_tensors([t]), eg.AdamWStep(**hyper, step=1))
+    assert torch.equal(t["param"].cpu(), want)
+    table = eg.AdamWTable(zeros(), n // 64, 64, eg.F32, zeros(), zeros())
+    ids = torch.arange(n // 64, dtype=torch.int32, device="cuda")
+    count = torch.tensor([n // 64], dtype=torch.int32, device="cuda")
+    eg.engram_adamw_rows(ctx, table, ids, count, n // 64, t["grad"], eg.AdamWStep(**hyper, step=1))
+    eg.engram_sync(ctx)
+    assert torch.equal(table.kept[0].cpu(), want)
