@@ -55,6 +55,8 @@ class TrainStep:
     All of a step, the library's calls and torch's alike, runs on it.
     """
 
+    ready = False  # whether the gradients are those of the last forward()
+
     def __init__(self, model, layer: int, embedding, head, tokens: int, *, kv_format=KV_BF16,
                  scale=None, norm=None):
         g = model.geom
@@ -136,7 +138,7 @@ class TrainStep:
         self._check_step(ids, windows, labels, T)
         if layer in self.model.outdated:
             raise ValueError("the layer's weights changed since it was bound: model.rebind(layer) first")
-        self.T, stream = T, self._on(stream)
+        self.T, self.ready, stream = T, False, self._on(stream)
         engram_embed(ctx, self.embedding, EMBED_BF16, self.vocab, self.d, ids, T, self.scale, self.hc,
                      self.hidden, stream)
         engram_hash(ctx, layer, windows, T, self.rows, stream)
@@ -182,6 +184,7 @@ class TrainStep:
         row_dim = self.model.geom["row_dim"]
         engram_embed_grad(ctx, self.model.rows(layer), row_dim, self.rows, T * self.model.nb, 1.0, 1,
                           self.demb, self.row_ids, self.row_count, self.row_grad, 0, self.ws, stream)
+        self.ready = True
 
 
 class AdamW:
@@ -276,7 +279,7 @@ class AdamW:
             self.lr.fill_(float(lr))
 
     def step(self, stream=None, rebind=True):
-        """One update with the gradients of the last backward().
+        """One update with the gradients of the last backward(), which has to be that of the last forward().
 
         The layer's next use needs what it keeps of its weights made again.  ``rebind``: wait for the
         update and bind the layer (and return what ``model.rebind`` does: True where what was captured
@@ -286,8 +289,8 @@ class AdamW:
         bound (``model.rebind(layer)``) before its next forward(), which refuses until then; such a
         step is not captured."""
         t = self.train
-        if t.T == 0:
-            raise ValueError("no backward() whose gradients could be used")
+        if not t.ready:
+            raise ValueError("no backward() of the last forward() whose gradients could be used")
         ctx, stream = t.model.ctx, t._on(stream)
         fp16 = t.model.fp16_operands(t.layer)
         with torch.cuda.stream(stream):

@@ -167,3 +167,24 @@ def test_a_captured_forward_holds_over_binds():
     assert same(replay(), eager())
     eg.engram_sync(s.ctx)
     s.close()
+
+
+def test_a_step_takes_the_gradients_of_the_last_forward():
+    """Neither buffers that no backward() wrote nor the gradients of a batch before."""
+    s, kept, step, opt, side, inputs = made(False)
+    weights = [x.clone() for x in (step.head, step.embedding, kept["wkv"])]
+    step.forward(*inputs[:3], side)
+    with pytest.raises(ValueError, match="backward"):
+        opt.step(side)
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 0
+    assert all(torch.equal(a, b) for a, b in zip(weights, (step.head, step.embedding, kept["wkv"])))
+    step.backward(*inputs, side)
+    opt.step(side)
+    step.forward(*inputs[:3], side)
+    with pytest.raises(ValueError, match="backward"):
+        opt.step(side)
+    torch.cuda.synchronize()
+    assert int(opt.steps) == 1
+    eg.engram_sync(s.ctx)
+    s.close()

@@ -275,3 +275,15 @@ def test_a_step_on_an_outdated_layer_is_refused():
     with pytest.raises(ValueError, match="rebind"):
         step.forward(torch.zeros(5, dtype=i32), torch.zeros(5, 4, dtype=i32), torch.zeros(5, dtype=i32))
     assert step.T == 0
+
+
+def test_an_optimizer_refuses_a_forward_without_its_backward():
+    from types import SimpleNamespace
+
+    from engram_gram_conditional_gb300.training import AdamW, TrainStep
+
+    opt = object.__new__(AdamW)  # (its buffers need a GPU; what is refused reaches none)
+    opt.train = object.__new__(TrainStep)
+    opt.train.model, opt.train.T = SimpleNamespace(ctx=None), 5
+    with pytest.raises(ValueError, match="backward"):
+        opt.step()
