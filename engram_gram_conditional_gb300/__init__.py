@@ -575,17 +575,61 @@ def _flat(name, x, n):
     return x.data_ptr()
 
 
+def _held(name, x, n, sizes):
+    """The address of a contiguous tensor of at least n values of `sizes` (a tuple) bytes each; other
+    buffers' as they are."""
+    if x is None or isinstance(x, int):
+        return x
+    if not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if x.numel() < n or x.element_size() not in sizes or not x.is_contiguous():
+        raise EngramError(EINVAL, f"{name}: {n} contiguous values of {' or '.join(map(str, sizes))} bytes expected, "
+                                  f"got {x.dtype} {list(x.shape)}")
+    return x.data_ptr()
+
+
+def _place(buffers, place=None):
+    """The index of the CUDA device that all tensors among `buffers` (and those of `place`) are on, None
+    where there are only addresses, -1 where one is elsewhere."""
+    for x in buffers:
+        if x is None or isinstance(x, int):
+            continue
+        at = x.get_device() if hasattr(x, "get_device") else -1 if isinstance(x, np.ndarray) else place
+        if place is None:
+            place = at
+        elif at != place:
+            return -1
+    return place
+
+
+_current_device = None  # torch's function, from the first call that has tensors on
+
+
+def _on_device(name, place):
+    """Refuses buffers that the kernels would not find on the current device."""
+    global _current_device
+    if place is None:
+        return
+    if _current_device is None:
+        import torch
+
+        _current_device = torch.cuda.current_device
+    if place < 0 or _current_device() != place:
+        raise EngramError(EINVAL, f"{name}: tensors on the current CUDA device expected")
+
+
 def grad_parts(parts):
     """engram_grad_norm's list from dicts: ``grad`` (a tensor, fp32 or BF16), and for the sparse
     gradient of a table ``count`` (a device uint32) and ``dim`` (values of a row).  The list
     keeps the tensors alive."""
     out = (GradPart * len(parts))()
     out.kept = [dict(p) for p in parts]
+    out.place = _place([x for p in parts for x in (p["grad"], p.get("count"))])
     for c, p in zip(out, parts):
         grad, dim = p["grad"], p.get("dim", 1)
         if grad.numel() % dim:
             raise EngramError(EINVAL, f"grad: rows of {dim} values expected, got {list(grad.shape)}")
-        c.grad, c.count = _flat("grad", grad, grad.numel()), _ptr(p.get("count"))
+        c.grad, c.count = _flat("grad", grad, grad.numel()), _held("count", p.get("count"), 1, (4,))
         c.n, c.dim, c.format = grad.numel() // dim, dim, _format(grad)
     return out
 
@@ -597,6 +641,7 @@ def engram_grad_norm_workspace_bytes(parts) -> int:
 
 def engram_grad_norm(ctx, parts, max_norm, d_norms, d_norm, d_factor, d_workspace, stream=None):
     """``parts``: grad_parts()'s list."""
+    _on_device("parts", getattr(parts, "place", None))
     _check(lib().engram_grad_norm(ctx, parts, len(parts), max_norm, _ptr(d_norms), _ptr(d_norm),
                                   _ptr(d_factor), _ptr(d_workspace), _stream(stream)))
 
@@ -607,6 +652,7 @@ def adamw_tensors(tensors):
     list keeps the tensors alive."""
     out = (AdamWTensor * len(tensors))()
     out.kept = [dict(t) for t in tensors]
+    out.place = _place([x for t in tensors for x in t.values() if not isinstance(x, float)])
     sizes = {t[name].element_size() for t in tensors for name in ("m", "v")}
     if len(sizes) > 1 or not sizes <= {1, 4}:
         raise EngramError(EINVAL, "m and v: all fp32, or all 8-bit codes")
@@ -624,37 +670,65 @@ def adamw_tensors(tensors):
     return out
 
 
+def _word(name, x, floating):
+    """The address of a device word: fp32, or a whole number of 32 bits."""
+    if x is None or not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if x.element_size() != 4 or x.is_floating_point() != floating or x.numel() < 1:
+        raise EngramError(EINVAL, f"{name}: {'fp32' if floating else 'int32'} expected, got {x.dtype} {list(x.shape)}")
+    return x.data_ptr()
+
+
 def AdamWStep(lr=0.0, beta1=0.9, beta2=0.999, eps=1e-8, step=0, seed=0, state_format=F32, d_lr=None,
               d_step=None, d_factor=None):
     """engram_adamw_step; d_lr, d_step and d_factor: device tensors (or addresses) or None."""
-    out = _AdamWStep(lr, beta1, beta2, eps, seed, _ptr(d_lr), _ptr(d_step), _ptr(d_factor), step,
-                     int(state_format))
+    out = _AdamWStep(lr, beta1, beta2, eps, seed, _word("d_lr", d_lr, True), _word("d_step", d_step, False),
+                     _word("d_factor", d_factor, True), step, int(state_format))
     out.kept = d_lr, d_step, d_factor
+    out.place = _place(out.kept)
     return out
+
+
+_SIZES = {F32: (4,), BF16: (2,), MXFP8: (1,)}
 
 
 def AdamWTable(table, rows, dim, table_format, m, v, scales=None, master=None, m_scales=None,
                v_scales=None, lr_scale=1.0, weight_decay=0.0):
     """engram_adamw_table; the buffers are device tensors (or addresses)."""
-    out = _AdamWTable(_ptr(table), _ptr(scales), _ptr(master), _ptr(m), _ptr(v), _ptr(m_scales),
-                      _ptr(v_scales), rows, dim, int(table_format), lr_scale, weight_decay)
+    n, one, four = rows * dim, (1,), (4,)
+    state = one if hasattr(m, "data_ptr") and m.element_size() == 1 else four
+    out = _AdamWTable(_held("table", table, n, _SIZES.get(table_format, (1, 2, 4))), _held("scales", scales, n // 32, one),
+                      _held("master", master, n, four), _held("m", m, n, state), _held("v", v, n, state),
+                      _held("m_scales", m_scales, n // 32, one), _held("v_scales", v_scales, n // 32, one),
+                      rows, dim, int(table_format), lr_scale, weight_decay)
     out.kept = table, scales, master, m, v, m_scales, v_scales
+    out.place = _place(out.kept)
+    out.state_format = None if not hasattr(m, "data_ptr") else MXFP8 if state is one else F32
     return out
+
+
+def _goes_with(step, out, name, buffers=()):
+    """Refuses a list or table whose states are not the step's, and buffers that are not on the device."""
+    kept = getattr(out, "state_format", None)
+    if step is not None and kept is not None and kept != step.state_format:
+        raise EngramError(EINVAL, f"state_format: the states of {name} have the other one")
+    place, other = getattr(out, "place", None), getattr(step, "place", None)
+    _on_device(name, _place(buffers, other if place is None else place if other is None or other == place else -1))
 
 
 def engram_adamw(ctx, tensors, step, stream=None):
     """``tensors``: adamw_tensors()'s list; ``step``: AdamWStep()."""
-    kept = getattr(tensors, "state_format", None)
-    if step is not None and kept is not None and kept != step.state_format:
-        raise EngramError(EINVAL, "state_format: the list's states have the other one")
+    _goes_with(step, tensors, "tensors")
     _check(lib().engram_adamw(ctx, tensors, len(tensors), None if step is None else C.byref(step),
                               _stream(stream)))
 
 
 def engram_adamw_rows(ctx, table, d_ids, d_count, n, d_grad, step, stream=None):
     """``table``: AdamWTable(); ``step``: AdamWStep()."""
-    _check(lib().engram_adamw_rows(ctx, None if table is None else C.byref(table), _ptr(d_ids),
-                                   _ptr(d_count), n, _ptr(d_grad),
+    _goes_with(step, table, "table, step and gradient", (d_ids, d_count, d_grad))
+    dim = 0 if table is None else table.dim
+    _check(lib().engram_adamw_rows(ctx, None if table is None else C.byref(table), _held("ids", d_ids, n, (4,)),
+                                   _held("count", d_count, 1, (4,)), n, _held("grad", d_grad, n * dim, (4,)),
                                    None if step is None else C.byref(step), _stream(stream)))
 
 

@@ -287,3 +287,56 @@ def test_an_optimizer_refuses_a_forward_without_its_backward():
     opt.train.model, opt.train.T = SimpleNamespace(ctx=None), 5
     with pytest.raises(ValueError, match="backward"):
         opt.step()
+
+
+def eight_rows(**bad):
+    f = torch.zeros
+    u8 = torch.uint8
+    return {**dict(table=f(10, 64, dtype=u8), rows=10, dim=64, table_format=eg.MXFP8, m=f(10, 64, dtype=u8),
+                   v=f(10, 64, dtype=u8), scales=f(10, 2, dtype=u8), master=f(10, 64), m_scales=f(10, 2, dtype=u8),
+                   v_scales=f(24, dtype=u8)), **bad}
+
+
+@pytest.mark.parametrize("bad", [dict(table=torch.zeros(10, 64)), dict(table=torch.zeros(9, 64, dtype=torch.uint8)),
+                                 dict(table=torch.zeros(10, 128, dtype=torch.uint8)[:, ::2]),
+                                 dict(table_format=eg.BF16), dict(table_format=eg.F32),
+                                 dict(scales=torch.zeros(19, dtype=torch.uint8)), dict(scales=torch.zeros(20)),
+                                 dict(master=torch.zeros(10, 64, dtype=torch.bfloat16)), dict(master=torch.zeros(639)),
+                                 dict(m=torch.zeros(10, 64)), dict(v=torch.zeros(10, 63, dtype=torch.uint8)),
+                                 dict(m=torch.zeros(10, 64, dtype=torch.int16), v=torch.zeros(10, 64, dtype=torch.int16)),
+                                 dict(m_scales=torch.zeros(19, dtype=torch.uint8)),
+                                 dict(v_scales=torch.zeros(20, dtype=torch.int16))])
+def test_a_table_refuses_buffers_that_do_not_go_together(bad):
+    assert eg.AdamWTable(**eight_rows()).state_format == eg.MXFP8
+    refused(eg.EINVAL, lambda: eg.AdamWTable(**eight_rows(**bad)))
+
+
+@pytest.mark.parametrize("bad", [dict(d_lr=torch.zeros(1, dtype=torch.float64)), dict(d_lr=torch.zeros(0)),
+                                 dict(d_step=torch.zeros(1)), dict(d_step=torch.zeros(1, dtype=torch.int64)),
+                                 dict(d_factor=torch.zeros(1, dtype=torch.bfloat16))])
+def test_a_step_refuses_words_of_another_type(bad):
+    refused(eg.EINVAL, lambda: eg.AdamWStep(**bad))
+
+
+def test_buffers_that_are_not_on_the_device_are_refused(ctx):
+    """Before a kernel gets their addresses."""
+    eight, i32 = step(state_format=eg.MXFP8), torch.int32
+    refused(eg.EINVAL, eg.engram_adamw, ctx, eg.adamw_tensors([good()]), eight)
+    refused(eg.EINVAL, eg.engram_adamw, ctx, (eg.AdamWTensor * 1)(tensor()), step(d_lr=torch.zeros(1)))
+    refused(eg.EINVAL, eg.engram_grad_norm, ctx, eg.grad_parts([dict(grad=torch.zeros(8))]), 1.0, A, A, A, A)
+    refused(eg.EINVAL, eg.engram_grad_norm, ctx, eg.grad_parts([dict(grad=torch.zeros(8, device="meta"))]), 1.0, A, A, A, A)
+    refused(eg.EINVAL, eg.grad_parts, [dict(grad=torch.zeros(8), count=torch.zeros(1, dtype=torch.int64))])
+    rows = eg.AdamWTable(**eight_rows())
+    refused(eg.EINVAL, eg.engram_adamw_rows, ctx, rows, A, A, 4, A, eight)
+    refused(eg.EINVAL, eg.engram_adamw_rows, ctx, rows, A, A, 4, A, step())  # (fp32 states)
+    refused(eg.EINVAL, eg.engram_adamw_rows, ctx, table(), torch.zeros(4, dtype=i32), A, 4, A, step())
+    refused(eg.EINVAL, eg.engram_adamw_rows, ctx, table(), A, np.zeros(1, np.int32), 4, A, step())
+
+
+@pytest.mark.parametrize("bad", [dict(ids=torch.zeros(3, dtype=torch.int32)), dict(ids=torch.zeros(4, dtype=torch.int64)),
+                                 dict(count=torch.zeros(1, dtype=torch.int64)), dict(grad=torch.zeros(4, 63)),
+                                 dict(grad=torch.zeros(4, 64, dtype=torch.bfloat16))])
+def test_rows_refuse_tensors_of_another_size(ctx, bad, monkeypatch):
+    monkeypatch.setattr(eg, "_on_device", lambda *a: None)
+    a = {**dict(ids=A, count=A, n=4, grad=A), **bad}
+    refused(eg.EINVAL, eg.engram_adamw_rows, ctx, table(), *a.values(), step())
