@@ -316,7 +316,7 @@ __device__ __forceinline__ void back_store(const NormBackArgs& a, char* res, cha
 template <int kVec, bool kWarp, bool kF32>
 __global__ void __launch_bounds__(kWarp ? kGroupThreads : row_threads(kVec, false)) k_norm_backward(NormBackArgs a) {
     __shared__ float sm[2][32][2];
-    extern __shared__ float dw_groups[];  // kWarp: [groups][lanes kVec 8], the groups' shares of dw
+    extern __shared__ __align__(16) float dw_groups[];  // kWarp: [groups][lanes kVec 8], the groups' shares of dw
     constexpr int kBytes = kF32 ? 4 : 2;
     pdl_launch_dependents();
     const Place p = place<kWarp>(a.lanes);
