@@ -670,8 +670,14 @@ engram_status engram_grad_norm(const engram_ctx* ctx, const engram_grad_part* pa
  * v by less than E4M3's neighbours are apart; to nearest it would stand still): 16 random
  * bits a value, those of Philox4x32-10 with key seed and counter (place / 8, number of the
  * tensor in the list, step), place the value's index in its tensor or table; the same
- * arguments give the same codes.  A positive root never takes code 0 (a v below fp32's normal
- * range counts as less than it is, down to 0).  Values stay in fp32's range: |factor grad| and |grad| below 1e19. */
+ * arguments give the same codes.  m and the root of one value are rounded with the same bits, and
+ * engram_adamw_rows counts as tensor 0: calls of one step that get one seed share their bits at equal
+ * numbers and places.  A positive root never takes code 0 (a v below fp32's normal range counts as
+ * less than it is, down to 0).  What 8 bits cost: a code's expectation is the value, but it stays
+ * within a step or two of E4M3 around it.  Under gradients of one size the root settles with a
+ * standard deviation of 15 % around its mean (fp32 states at beta2 0.999: 1.6 %), and m is
+ * off by 9 % of its own size (beta1 0.9), both whatever beta2.
+ * Values stay in fp32's range: |factor grad| and |grad| below 1e19. */
 typedef struct engram_adamw_step {
     double lr, beta1, beta2, eps; /* betas in [0, 1), eps a positive normal fp32 number */
     uint64_t seed;
