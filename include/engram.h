@@ -176,7 +176,8 @@ engram_status engram_layer_set_multipliers(engram_ctx* ctx, int layer, const uin
  * allocates the context's device word at first use, scans the table's scale
  * exponents and wkv's magnitude, builds the FP16 copy of wkv when the FP16
  * operand path applies (engram_layer_info), keeps the product w_q w_k (the
- * gate uses the two only through it: bind again after changing them) and
+ * gate uses the two only through it: bind again after changing them, or see
+ * engram_layer_refresh) and
  * encodes the TMA descriptors.  It synchronises the device.
  * Launches of the layer that were captured into a graph hold what the bind gave them: the arrays'
  * and the copies' addresses, which a bind to the same arrays leaves as they are, and on the FP16
@@ -188,8 +189,8 @@ engram_status engram_layer_bind(engram_ctx* ctx, int layer, const engram_layer_w
  * w_q and w_k.  It allocates nothing, does not synchronise and may be captured: the last part of a
  * training step whose graph is replayed.  Everything else that a layer on BF16 operands uses it
  * reads from the bound arrays.  A layer on FP16 operands (engram_layer_info's fp16_operands) also
- * holds a copy of wkv and the exponents of its table: ENGRAM_EUNSUPPORTED; it is bound again, or
- * was to be bound with ENGRAM_BIND_BF16_OPERANDS. */
+ * holds a copy of wkv and the exponents of its table: ENGRAM_EUNSUPPORTED.  It is bound again
+ * instead, or has been bound with ENGRAM_BIND_BF16_OPERANDS. */
 engram_status engram_layer_refresh(const engram_ctx* ctx, int layer, void* stream);
 
 /* Fill rows [row_begin, row_end) of a table with its deterministic contents:
@@ -644,7 +645,8 @@ engram_status engram_norm_backward(const engram_ctx* ctx, const void* d_sum, int
  * together, d_factor max_norm / norm where the norm is above max_norm, else 1 (each may be
  * NULL).  Where the norm is not finite the factor is NaN, which engram_adamw and
  * engram_adamw_rows take as a step to leave out.  Squares are computed and first summed
- * in fp32: values above about 1e18 count as not finite.
+ * in fp32: values above about 1e18 count as not finite, those below about 1e-19 as less than they
+ * are, down to 0.
  * d_workspace: engram_grad_norm_workspace_bytes(parts, count) bytes, at least as many as for
  * a shorter list or one with smaller parts (only n and dim count).  grad 16-byte aligned. */
 typedef struct engram_grad_part {
@@ -719,8 +721,8 @@ engram_status engram_adamw(const engram_ctx* ctx, const engram_adamw_tensor* ten
  * table [rows][dim]: fp32; BF16, with an fp32 master [rows][dim] or without; or MXFP8 codes
  * uint8 with scales uint8 [rows][dim / 32] (rounded to nearest even) and a master.  m, v fp32
  * [rows][dim], or uint8 with m_scales, v_scales uint8 [rows][dim / 32].  dim: a multiple of 8
- * (of 32 where anything is MXFP8) up to 65,536.  A layer that is bound to the table is bound
- * again before its next use where an MXFP8 table's scales may have changed their range.
+ * (of 32 where anything is MXFP8) up to 65,536.  A layer on FP16 operands that is bound to the
+ * table is bound again before its next use: the scales may have changed their range.
  * A context with no bound layer gets its device word here: make the first call before a
  * capture. */
 typedef struct engram_adamw_table {
