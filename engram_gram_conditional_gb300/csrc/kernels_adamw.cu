@@ -8,9 +8,9 @@
 // What is read at a time has to lie together for HBM to reach a copy's rate: blocks take
 // short stretches and follow one another in order, instead of staying and drifting apart.
 // Measured, against the bytes at a copy's 6.79 TB/s: wkv (157M values) with masters and
-// fp32 states 652 us (1.00); wkv and head (820M, BF16) with 8-bit states 1,227 us (1.00);
-// 4,915 rows of 5,120 with masters and fp32 states 114 us (0.97); 1.08M rows of 256, MXFP8
-// with masters, 8-bit states 724 us (0.97); norms of 1.74 GB of gradients 244 us (1.05).
+// fp32 states 648 us (1.00); wkv and head (820M, BF16) with 8-bit states 1,281 us (0.95);
+// 4,915 rows of 5,120 with masters and fp32 states 117 us (0.95); 1.08M rows of 256, MXFP8
+// with masters, 8-bit states 726 us (0.96); norms of 1.74 GB of gradients 246 us (1.04).
 //
 // 8-bit states are MXFP8 blocks of m and of r = sqrt(v).  A step moves r by a part of
 // (1 - b2) / 2, 0.05 % at b2 = 0.999, while E4M3's neighbours are 6 to 12 % apart: to
@@ -67,7 +67,7 @@ __device__ __forceinline__ void step1(const AdamwStep& h, const Rates& q, float 
 
 // A thread holds 16 values, half a block of 32, in pairs: 10 bytes a value leave 54 of an
 // SM's issue slots for it, of which a thread's 8 values one by one took 87; two values an
-// instruction, and 16 to share what a block costs, take 37.
+// instruction, and 16 to share what a block costs, take 42, and the slots are two thirds busy.
 
 // 1 / sqrt(v) and 1 / v, off by up to 2^-22 and 2^-23 of themselves.
 __device__ __forceinline__ float inverse_root(float v) {
@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kThreads)
 // 8-bit states.  A block takes some neighbouring cells of kMxThreads x 16 values, tensor by
 // tensor: within one nothing is asked again and addresses only grow, and while a block works
 // on a cell the next one's values are on their way to shared memory.
-// 61M values: 256 threads, two blocks of an SM and two stages 100 us; 128 threads and four
-// blocks 105; three blocks (fewer registers, spills) 112; three stages 102.
+// 61M values, with an approximate root: 256 threads, two blocks of an SM and two stages 100 us; 128
+// threads and four blocks 105; three blocks (fewer registers, spills) 112; three stages 102.
 constexpr int kMxThreads = 256;
 constexpr int kStages = 2;
 constexpr int kCell = kMxThreads * 16;
@@ -498,8 +498,8 @@ __device__ __noinline__ void last_cell(const AdamwStep& h, const Rates& q, const
     }
 }
 
-// 820M values: 8 cells a block 1,219 us, 4 (their beginnings show) 1,303; 61M: 100, 4 104, 16
-// (an uneven last wave) 107, blocks that stay 104.
+// 820M values, with an approximate root: 8 cells a block 1,219 us, 4 (their beginnings show) 1,303;
+// 61M: 100, 4 104, 16 (an uneven last wave) 107, blocks that stay 104.
 constexpr unsigned kCellsPerBlock = 8;
 constexpr int kMxBlocks = 2;  // of an SM, at 128 registers a thread
 

@@ -13,10 +13,10 @@
 // of 4 x 5,120: 78 us, 124 without).  Sums are fp32.
 //
 // Measured, against the bytes at a copy's 6.79 TB/s: 50,032 x 5,120 BF16 with residual
-// 298 us (1.01), 20,000 rows to 8 bits 109 (0.97), 2,048 rows of 4 branches 19 (0.97),
-// backward 8,192 rows into 4 branches 94 (0.92), 16,000 rows into one 112 (0.86), 256 rows
+// 298 us (1.01), 20,000 rows to 8 bits 113 (0.94), 2,048 rows of 4 branches 19 (0.97),
+// backward 8,192 rows into 4 branches 95 (0.92), 16,000 rows into one 109 (0.89), 256 rows
 // to 8 bits 3.4 (0.4: latency).  The backward pass is held back by its rows' chain of sum,
-// barrier and second use, with one row of an SM at a time in most of its steps.
+// barrier and second use: a block has one row, or a pair, in work at a time.
 #include <algorithm>
 
 #include "mx8.cuh"
@@ -582,7 +582,7 @@ Walk walk_of(const Shape& sh, int64_t n, int per_sm, int stages, int64_t bytes, 
     return {(int)std::max<int64_t>(1, std::min(groups, direct)), 0, 0};
 }
 
-// 8,192 rows of 4 x 5,120 (40 KB): one block and three stages 76 us, two and two 84; 20,000
+// 8,192 rows of 4 x 5,120 (40 KB): one block and three stages 78 us, two and two 8 more; 20,000
 // rows of 2 x 5,120: two blocks and two stages 127 us, three stages 137, one block and four
 // 131; an 8-bit output: two blocks and three stages 115, two stages 123.
 Walk norm_walk(const Shape& sh, int64_t n, bool mx, int64_t bytes) {
