@@ -80,7 +80,8 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 // pdl_launch_dependents (or exited); pdl_wait then blocks until that kernel
 // has finished and its writes are visible.  Every kernel launched this way
 // calls pdl_wait before it touches memory that earlier work in the stream
-// writes.
+// writes, but for a layer's weights and windows, which some read at once: a
+// kernel that writes those does not call pdl_launch_dependents.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

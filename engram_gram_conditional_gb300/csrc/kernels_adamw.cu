@@ -34,6 +34,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// The steps' kernels do not call pdl_launch_dependents: the layer's kernels read wkv and the table
+// before they wait for the kernel before them, as nothing but these (and a bind) writes them.
+
 // ---- the element's step -------------------------------------------------------------------
 
 // A step's numbers as an element needs them.
@@ -312,7 +315,6 @@ template <int kN>
 __global__ void __launch_bounds__(kThreads)
     k_adamw(const __grid_constant__ AdamwStep h, const __grid_constant__ AdamwTensors<kN> list, int count,
             int iters) {
-    pdl_launch_dependents();
     const int k = last_before(list.first, count, blockIdx.x);
     const AdamwTensor& t = list.t[k];
     const uint64_t n = t.n;
@@ -508,7 +510,6 @@ __global__ void __launch_bounds__(kMxThreads, kMxBlocks)
     k_adamw_mx(const __grid_constant__ AdamwStep h, const __grid_constant__ AdamwTensors<kN> list, int count,
                uint32_t cells, uint32_t per_block) {
     extern __shared__ uint4 stages[];
-    pdl_launch_dependents();
     pdl_wait();
     const Rates q = rates_of(h);
     if (q.factor != q.factor) return;  // the gradients are not finite: no step
@@ -547,7 +548,6 @@ __device__ __forceinline__ bool goes(const AdamwRows& a, uint64_t i, uint32_t id
 template <bool kTableMx>
 __global__ void __launch_bounds__(kThreads)
     k_adamw_rows(const __grid_constant__ AdamwStep h, const __grid_constant__ AdamwRows a) {
-    pdl_launch_dependents();
     const uint32_t V = a.dim / 4;
     const bool pf32 = a.kind & kParamF32, master = a.kind & kMaster;
     float* const param = master ? a.master : static_cast<float*>(a.table);
@@ -626,7 +626,6 @@ __global__ void __launch_bounds__(kMxThreads, kMxBlocks)
     using P = WarpValues<kP>;
     using G = WarpValues<true>;
     constexpr int kPieces = pieces_of(kP, true), kG = P::kPieces * 32, kM = kG + G::kPieces * 32, kV = kM + 32;
-    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t V = a.dim / 16;
     char* const param = static_cast<char*>(kMasters ? (void*)a.master : a.table);

@@ -190,8 +190,8 @@ __global__ void k_gather(const uint32_t* __restrict__ rows, int64_t T, int nb, i
 // row is read whole: row_dim / 16 lanes per row, 16 codes and their scale per
 // lane; the first lane of a row hashes its (token, bucket) pair.
 // Launched as a programmatic dependent: the hashing and the row loads (of
-// windows and table, which no kernel of the stream writes) may overlap the
-// kernel before; every thread waits for it (pdl_wait) before its first store,
+// windows and table; what writes those, an optimizer's step among it, lets no
+// kernel start before its end) may overlap the kernel before; every thread waits for it (pdl_wait) before its first store,
 // since e may still be read by the GEMM of the previous call.  Block 0 then
 // also zeroes n_clear words at `clear` (the stream-K flags of the GEMM after).
 // kRaw: the rows come not from the table but from raw MXFP8 rows that the

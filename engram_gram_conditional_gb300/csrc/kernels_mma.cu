@@ -580,8 +580,9 @@ k_mma(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorM
     // kernel before it in the stream (the gather that writes the A operand, or
     // the previous call) still runs.  The roles that touch memory earlier work
     // writes wait for it (pdl_wait) first: the A producer and the epilogue.
-    // The wkv producer does not: wkv is written only at bind, so the first wkv
-    // stages load while the gather finishes.  The kernel after this one (the
+    // The wkv producer does not: what writes wkv (a bind, an optimizer's step)
+    // lets no kernel start before its end, so the first wkv stages load while
+    // the gather finishes.  The kernel after this one (the
     // gate) may be scheduled as CTAs of this one exit.
     pdl_launch_dependents();
 

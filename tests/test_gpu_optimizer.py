@@ -188,3 +188,45 @@ def test_a_step_takes_the_gradients_of_the_last_forward():
     assert int(opt.steps) == 1
     eg.engram_sync(s.ctx)
     s.close()
+
+
+@pytest.mark.parametrize("states", ["f32", "mxfp8"])
+def test_what_follows_an_update_on_the_stream_reads_the_new_weights(states):
+    """Kernels of the layer load wkv and the table before they wait for the kernel before them: the step's
+    kernels let them start only when they are done."""
+    s, kept, embedding, head, norm = step_model(False)
+    T, mx = 64, states == "mxfp8"
+    side = torch.cuda.Stream()
+    dev = dict(device="cuda")
+    emb = torch.randn(T, s.K, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    windows = step_inputs(s, T, 2)[1]
+    ws = torch.empty(eg.engram_forward_staged_workspace_bytes(s.ctx, T), dtype=torch.uint8, **dev)
+    wkv, rows, dim = kept["wkv"].view(torch.bfloat16), s.rows(0), s.geom["row_dim"]
+    table = kept["table"].view(torch.bfloat16)[:rows * dim]
+
+    def state(n):
+        if not mx:
+            return dict(m=torch.zeros(n, **dev), v=torch.zeros(n, **dev))
+        return {k: torch.zeros(n if k in "mv" else n // 32, dtype=torch.uint8, **dev) for k in ("m", "v", "m_scales", "v_scales")}
+
+    fmt = eg.MXFP8 if mx else eg.F32
+    dense = eg.adamw_tensors([dict(param=wkv, grad=torch.ones_like(wkv), **state(wkv.numel()))])
+    rows_table = eg.AdamWTable(table, rows, dim, eg.BF16, **state(rows * dim))
+    ids = torch.arange(rows, dtype=torch.int32, **dev)
+    count, grad = torch.tensor([rows], dtype=torch.int32, **dev), torch.ones(rows, dim, **dev)
+    got = [torch.empty(T, s.N, **dev) for _ in range(4)]
+    torch.cuda.synchronize()
+    for i in range(1, 21):
+        step = eg.AdamWStep(lr=0.5, step=i, state_format=fmt)  # (every weight moves by 0.5)
+        eg.engram_adamw(s.ctx, dense, step, side)
+        eg.engram_project(s.ctx, 0, emb, T, got[0], side)
+        torch.cuda.synchronize()
+        eg.engram_project(s.ctx, 0, emb, T, got[1], side)
+        eg.engram_adamw_rows(s.ctx, rows_table, ids, count, rows, grad, step, side)
+        eg.engram_prepass(s.ctx, 0, windows, T, got[2], eg.KV_F32, ws, side)
+        torch.cuda.synchronize()
+        eg.engram_prepass(s.ctx, 0, windows, T, got[3], eg.KV_F32, ws, side)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], got[1]) and torch.equal(got[2], got[3]), i
+    eg.engram_sync(s.ctx)
+    s.close()
