@@ -87,7 +87,7 @@ __device__ __forceinline__ float inverse(float v) {
 // Newton's from s = v y, y about 1 / sqrt(v): s + (v - s^2) y / 2, whose remainder an fma gives
 // exactly (Markstein, IBM J. Res. Dev. 34, 1990).  What is then rounded is off by 2^-43 of the root:
 // it is the nearest fp32 number but for one value in some 10^5.  Codes and scales are made of it: of
-// 1.02 billion values one code differs from those of rounded roots; with an approximate root 122 and
+// 276M values one code differs from those of rounded roots; with an approximate root 122 and
 // two blocks' scales did.  820M BF16 values take 1,283 us (the approximate root 1,237, sqrtf 1,403),
 // 61M 106 (102, 117); rows and tensors with masters what they took.
 __device__ __forceinline__ f32x2 root2(f32x2 v) {

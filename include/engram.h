@@ -717,7 +717,9 @@ engram_status engram_adamw(const engram_ctx* ctx, const engram_adamw_tensor* ten
  * d_count, d_grad).  The other rows, their states and their decay stay as they are; the
  * corrections go by the step's number, not by how often a row had a gradient.
  * ids ascend: an id >= rows, or one that is not above the id before it, is left out and sets
- * the error word (ENGRAM_EBOUNDS at the next engram_sync).
+ * the error word (ENGRAM_EBOUNDS at the next engram_sync).  Only neighbours are compared: a row that
+ * comes again further behind, after a descent, is stepped by both at once, and its values are
+ * then undefined.
  * table [rows][dim]: fp32; BF16, with an fp32 master [rows][dim] or without; or MXFP8 codes
  * uint8 with scales uint8 [rows][dim / 32] (rounded to nearest even) and a master.  m, v fp32
  * [rows][dim], or uint8 with m_scales, v_scales uint8 [rows][dim / 32].  dim: a multiple of 8
